@@ -79,6 +79,7 @@ typedef enum {
 #define MOE_DEVERR_BAD_SLOT 0x2u     /* slot_table gave a slot outside [0, n_slots)     */
 #define MOE_DEVERR_NONFINITE 0x4u    /* a router logit was NaN/Inf; top-k may be short  */
 #define MOE_DEVERR_TIMEOUT 0x8u      /* a bounded device wait gave up                   */
+#define MOE_DEVERR_BAD_RANGE 0x10u   /* a sequence's rows lie outside the call's: skipped */
 
 typedef struct {
   int32_t hidden;       /* H: model width (multiple of 64)                                 */
@@ -352,6 +353,82 @@ MOE_API moe_status moe_gdn_decode_step(const moe_gdn_shape* shape, int32_t B, fl
 MOE_API moe_status moe_gdn_decode_step_ex(const moe_gdn_shape* shape, int32_t B, float* state, const void* q,
                                           const void* k, const void* v, const float* g, const float* beta,
                                           void* out, int32_t flags, void* stream);
+
+/*
+ * moe_gdn_prefill -- the gated delta rule of moe_gdn_decode_step over whole prompts: n_seqs
+ * packed sequences of any lengths, every token in order, the state after the last one
+ * returned (a prompt, or the next piece of one; the decode steps go on from state_out).
+ *   n_seqs     1..65536
+ *   T          token rows of q, k, v, g, beta and out (>= 0)
+ *   offsets    (dev) int32 [n_seqs + 1]: sequence s is the rows offsets[s] .. offsets[s+1]-1,
+ *              0 <= offsets[0] <= offsets[1] <= ... <= T; a sequence may be empty
+ *   state_in   (dev) fp32 [n_seqs, H_v, d_v, d_k]: the states to start from, or NULL (zeros)
+ *   state_out  (dev) fp32 [n_seqs, H_v, d_v, d_k] out: the states after each sequence's last
+ *              token (an empty sequence: its starting state).  It may be state_in itself, but
+ *              must not overlap it otherwise
+ *   q, k       (dev) bf16 [T, H_k, d_k];  v (dev) bf16 [T, H_v, d_v]
+ *   g          (dev) fp32 [T, H_v] log decay (<= 0 for a decay; -inf forgets the state)
+ *   beta       (dev) fp32 [T, H_v]
+ *   out        (dev) bf16 [T, H_v, d_v] (round to nearest even of the fp32 value)
+ *   ws         (dev) workspace of ws_bytes >= moe_gdn_prefill_workspace_size(shape, n_seqs, T)
+ * Shapes as moe_gdn_decode_step.  Rows of out that belong to no sequence are left as they
+ * were.  A sequence whose range is out of order or outside [0, T] (offsets[s+1] < offsets[s],
+ * offsets[s+1] > T, or offsets[s] below an earlier offset) is left out, its rows of out and
+ * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  Deterministic: the same inputs
+ * give the same bits, whatever the other sequences of the call are.
+ */
+MOE_API moe_status moe_gdn_prefill_workspace_size(const moe_gdn_shape* shape, int32_t n_seqs, int32_t T,
+                                                  size_t* bytes);
+MOE_API moe_status moe_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs, int32_t T, const int32_t* offsets,
+                                   const float* state_in, float* state_out, const void* q, const void* k,
+                                   const void* v, const float* g, const float* beta, void* out, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* Causal softmax attention with grouped heads: the other quarter of the hybrid model's   */
+/* layers («Paquets Swiftlet 80B Qwen dans Mac…», paragraph 6: three quarters are linear  */
+/* attention), over whole prompts, pieces of prompts after their history, or single tokens.*/
+/* ------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t n_q_heads;   /* H_q: query heads                                                   */
+  int32_t n_kv_heads;  /* H_kv: key/value heads (query head h reads key head                 */
+                       /*       h / (H_q / H_kv); H_q / H_kv a whole number up to 64)        */
+  int32_t d;           /* head width: 64 or 128                                              */
+} moe_attn_shape;
+
+/*
+ * moe_attn_forward -- out_i = sum_j softmax_j(scale * q_i . k_j) v_j per sequence and head.
+ * The queries of a sequence are its last tokens: with n queries and a length of len keys,
+ * query i (0..n-1) sees the keys 0 .. len - n + i.  A whole prompt has len = n; a piece of a
+ * prompt, or one new token, has the keys before it in the cache.
+ *   n_seqs    1..65536
+ *   T         query rows of q and out (>= 0)
+ *   q_offsets (dev) int32 [n_seqs + 1]: sequence s has the query rows q_offsets[s] ..
+ *             q_offsets[s+1]-1, in order and within [0, T]; a sequence may have none
+ *   kv_begin  (dev) int32 [n_seqs]: row of k and v that holds the sequence's first key
+ *   kv_len    (dev) int32 [n_seqs]: its keys, 0 .. max_kv
+ *             Both NULL: k and v are packed like q (whole prompts); then kv_rows >= T and
+ *             max_kv bounds the prompts' lengths
+ *   max_kv    upper bound of every kv_len, known to the caller (>= 0)
+ *   q         (dev) bf16 [T, H_q, d];  k, v (dev) bf16 [kv_rows, H_kv, d]
+ *   kv_rows   rows of k and v (>= 0); rows that belong to no sequence are not used, whatever
+ *             they hold
+ *   scale     factor of the scores (finite), usually 1 / sqrt(d)
+ *   out       (dev) bf16 [T, H_q, d] (round to nearest even)
+ *   ws        (dev) workspace of ws_bytes >= moe_attn_workspace_size(shape, n_seqs, T, max_kv)
+ * A query that sees no key (len < n) gets zeros.  Rows of out that belong to no sequence are
+ * left as they were.  A sequence whose query rows are out of order or outside [0, T], or whose
+ * keys lie outside [0, kv_rows) or number more than max_kv, is left out, its rows of out
+ * untouched, and MOE_DEVERR_BAD_RANGE is set.  Sequences may share keys.  A key's value of
+ * infinity or NaN reaches the queries that see it, and may reach queries before it within 128
+ * keys of it.  Deterministic: the same inputs and the same call sizes give the same bits.
+ */
+MOE_API moe_status moe_attn_workspace_size(const moe_attn_shape* shape, int32_t n_seqs, int32_t T, int32_t max_kv,
+                                           size_t* bytes);
+MOE_API moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_seqs, int32_t T, const int32_t* q_offsets,
+                                    const int32_t* kv_begin, const int32_t* kv_len, int32_t max_kv, const void* q,
+                                    const void* k, const void* v, int32_t kv_rows, float scale, void* out, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------ */
 /* Bounded slot pool with LFU + recency eviction («Paquets Swiftlet…» paragraph 5;       */

@@ -21,7 +21,7 @@ MOE_OK = 0
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID", -2: "MOE_ERR_CUDA", -3: "MOE_ERR_CAPACITY",
           -4: "MOE_ERR_NOT_RESIDENT", -5: "MOE_ERR_UNSUPPORTED", -6: "MOE_ERR_TIMEOUT",
           -7: "MOE_ERR_DEVICE", -8: "MOE_ERR_IO"}
-DEVERR_BAD_EXPERT, DEVERR_BAD_SLOT, DEVERR_NONFINITE, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_BAD_EXPERT, DEVERR_BAD_SLOT, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_BAD_RANGE = 1, 2, 4, 8, 16
 
 
 class MoeError(RuntimeError):
@@ -57,6 +57,10 @@ class moe_gdn_shape(ctypes.Structure):
                 ("d_v", ctypes.c_int32)]
 
 
+class moe_attn_shape(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
@@ -79,6 +83,14 @@ _SIGS = {
     "moe_gdn_decode_step": (ctypes.c_int, [ctypes.POINTER(moe_gdn_shape), _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_gdn_decode_step_ex": (ctypes.c_int, [ctypes.POINTER(moe_gdn_shape), _I32, _P, _P, _P, _P, _P, _P, _P, _I32,
                                               _P]),
+    "moe_gdn_prefill_workspace_size": (ctypes.c_int, [ctypes.POINTER(moe_gdn_shape), _I32, _I32,
+                                                      ctypes.POINTER(_SZ)]),
+    "moe_gdn_prefill": (ctypes.c_int, [ctypes.POINTER(moe_gdn_shape), _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                       _P, _SZ, _P]),
+    "moe_attn_workspace_size": (ctypes.c_int, [ctypes.POINTER(moe_attn_shape), _I32, _I32, _I32,
+                                               ctypes.POINTER(_SZ)]),
+    "moe_attn_forward": (ctypes.c_int, [ctypes.POINTER(moe_attn_shape), _I32, _I32, _P, _P, _P, _I32, _P, _P, _P, _I32,
+                                        ctypes.c_float, _P, _P, _SZ, _P]),
     "moe_pool_create": (ctypes.c_int, [ctypes.POINTER(moe_shape), _I32, _P, _P, _P, ctypes.POINTER(_P)]),
     "moe_pool_create_file": (ctypes.c_int, [ctypes.POINTER(moe_shape), _I32, ctypes.c_char_p, _I32, _P, _P,
                                             ctypes.POINTER(_P)]),
@@ -265,6 +277,35 @@ def moe_gdn_decode_step(shape, B, state, q, k, v, g, beta, out, stream=None, fla
     else:
         _check(lib().moe_gdn_decode_step(ctypes.byref(shape), B, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                          _ptr(beta), _ptr(out), _stream(stream)))
+
+
+def moe_gdn_prefill_workspace_size(shape, n_seqs: int, T: int) -> int:
+    n = _SZ()
+    _check(lib().moe_gdn_prefill_workspace_size(ctypes.byref(shape), n_seqs, T, ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_gdn_prefill(shape, n_seqs, T, offsets, state_in, state_out, q, k, v, g, beta, out, ws, stream=None):
+    """The gated delta rule over n_seqs packed prompts (state_in None: from zero states; state_out
+    may be state_in)."""
+    _check(lib().moe_gdn_prefill(ctypes.byref(shape), n_seqs, T, _ptr(offsets), _ptr(state_in), _ptr(state_out), _ptr(q),
+                                 _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(out), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_attn_workspace_size(shape, n_seqs: int, T: int, max_kv: int) -> int:
+    n = _SZ()
+    _check(lib().moe_attn_workspace_size(ctypes.byref(shape), n_seqs, T, max_kv, ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_attn_forward(shape, n_seqs, T, q_offsets, kv_begin, kv_len, max_kv, q, k, v, kv_rows, scale, out, ws,
+                     stream=None):
+    """Causal attention of packed queries over their sequences' keys (kv_begin, kv_len None: whole
+    prompts, keys packed like the queries)."""
+    _check(lib().moe_attn_forward(ctypes.byref(shape), n_seqs, T, _ptr(q_offsets), _ptr(kv_begin), _ptr(kv_len), max_kv,
+                                  _ptr(q), _ptr(k), _ptr(v), kv_rows, scale, _ptr(out), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def moe_pool_create(shape, n_slots, host_blobs, dev_pool, dev_slot_table) -> int:

@@ -26,6 +26,7 @@ constexpr uint32_t kErrBadExpert = 0x1u;
 constexpr uint32_t kErrBadSlot = 0x2u;
 constexpr uint32_t kErrNonFinite = 0x4u;
 constexpr uint32_t kErrTimeout = 0x8u;
+constexpr uint32_t kErrBadRange = 0x10u;
 
 // ---------------------------------------------------------------------------------------
 // Fixed-stride expert blob: nine 256-byte aligned sections (gate/up/down codes, then

@@ -68,3 +68,27 @@ def gdn_steps(S: np.ndarray, q, k, v, g, beta):
         S, o = gdn_step(S, q[t], k[t], v[t], g[t], beta[t])
         outs.append(o)
     return S, np.stack(outs)
+
+
+def gdn_prompt(S: np.ndarray, q, k, v, g, beta):
+    """All T tokens of one sequence, the heads at once (the recurrence of gdn_step with
+    u = S k^ written out).  q, k [T, H_k, d_k], v [T, H_v, d_v], g, beta [T, H_v].
+    Returns (S after the last token, o [T, H_v, d_v], size [T, H_v, d_v], S_size [H_v, d_v]):
+    size is a bound of what o is a sum of, with |k^|, |q^| sqrt(d_k) <= 1:
+    m_t = alpha m_{t-1} + |write_t| from m_0 = the rows' largest |S| times sqrt(d_k), over
+    sqrt(d_k); S_size = m after the last token."""
+    S = np.array(S, dtype=np.float64)
+    Hv, dv, dk = S.shape
+    T = len(q)
+    head = np.arange(Hv) // (Hv // k.shape[1])
+    qn, kn = l2_normalize(q)[:, head] / np.sqrt(dk), l2_normalize(k)[:, head]
+    o, size = np.empty((T, Hv, dv)), np.empty((T, Hv, dv))
+    m = np.abs(S).max(-1) * np.sqrt(dk)
+    for t in range(T):
+        S *= np.exp(np.asarray(g[t], dtype=np.float64))[:, None, None]
+        write = np.asarray(beta[t])[:, None] * (v[t] - np.einsum("hvd,hd->hv", S, kn[t]))
+        S += write[:, :, None] * kn[t][:, None, :]
+        o[t] = np.einsum("hvd,hd->hv", S, qn[t])
+        m = np.exp(np.asarray(g[t], dtype=np.float64))[:, None] * m + np.abs(write)
+        size[t] = m / np.sqrt(dk)
+    return S, o, size, m
