@@ -1,15 +1,42 @@
 // Causal softmax attention with grouped heads over packed sequences (moe_attn_forward), sm_100a.
 //
-//     out_i = sum_j p_ij v_j,  p_ij = e^{x_ij - m_i} / sum_j e^{x_ij - m_i},  x_ij = scale q_i.k_j
+//     out_i = sum_j p_ij v_j,  p_ij = 2^{x_ij - m_i} / sum_j 2^{x_ij - m_i},  x_ij = scale log2(e) q_i.k_j
 //
 // over the keys j <= len - n + i of the query's sequence, in one pass over the keys with the
-// running maximum m_i and sum (a new maximum rescales what was summed before).
+// running maximum m_i and sum.
+//
+// A work unit is one key head and a block of up to 2 * PT query positions, PT = 128 / G with G
+// the query heads of a key head: the rows of a tile are (position, head of the group) pairs, so
+// a tile of 128 rows holds every query that shares the key head's keys at PT positions.  (One
+// head and 128 positions a tile would fill only G-th part of the rows for single tokens, and
+// mask more of the diagonal.)  The block's two tiles A and B share every key and value tile of
+// 128 rows:
+//
+//   k_attn_plan     one CTA: checks the sequences, cuts them into blocks, long blocks into
+//                   pieces of keys when the call has fewer blocks than would fill the GPU, and
+//                   orders the units by their number of key tiles, longest first
+//   k_attn<D>       persistent, one CTA per SM:
+//     warps 0-3, 4-7  softmax of tile A, B: a thread owns a row.  S from TMEM, running maximum and
+//                     sum, P as bf16 back into TMEM over S, O rescaled when a maximum rises by
+//                     more than 2^8, the end of the unit (O / sum, or the piece's O, m, sum)
+//     warp 8          lane 0 issues the MMAs: S = Q K^T (operands in shared memory), O += P V
+//                     (P in TMEM), alternating between the tiles so that one tile's softmax
+//                     overlaps the other's products
+//     warp 9          Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
+//   k_attn_join     joins the pieces of blocks that were cut
+//
+// What is rounded: P to bf16 (the tensor core's operand; one half step, 2^-8, of each weight),
+// and the result.  S, O, m and the sums are fp32.  A maximum may lag the true one by up to 2^8:
+// P keeps its relative precision and the fp32 sums their range.
 #include "../../include/moe.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "kernels.cuh"
 #include "seqs.cuh"
 #include "sync.cuh"
+#include "tc.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace moe {
@@ -19,26 +46,72 @@ struct AttnSeq {
   int kv0, len;   // first key row and keys
 };
 
+// A block of query positions of one sequence and a range of its key tiles (every key head is a
+// unit of its own).
+struct alignas(16) AttnUnit {
+  int row, npos;  // first query row, positions
+  int kv0, len;   // the sequence's keys
+  int seen;       // keys that the block's first position sees (0 or less: none); the next sees one more
+  int kt0, kt1;   // key tiles
+  int slot;       // -1, or the piece's place among the partial results
+};
+struct alignas(16) AttnRec {  // a block cut into pieces
+  int row, npos, seen, slot, pieces;
+};
+struct AttnHdr {
+  int n_units, n_recs;
+};
+
+constexpr int kAttnTile = 128;     // rows of a query tile and of a key tile
+constexpr int kAttnFill = 296;     // pieces aimed at: two per SM
+constexpr int kAttnMinPiece = 4;   // key tiles of a piece at least
+constexpr int kAttnMaxSlots = 2 * kAttnFill;
+
 struct AttnArgs {
-  int n_seqs, T, Hq, Hkv, d, max_kv, kv_rows;
-  float scale;
+  int n_seqs, T, Hq, Hkv, G, d, PT, max_kv, kv_rows, rows_slot;
+  float scale_log2;  // scale * log2(e)
   const int32_t *offsets, *kv_begin, *kv_len;
-  const uint16_t *q, *k, *v;
   uint16_t* out;
   Ctrl* ctrl;
-  AttnSeq* seqs;  // [n_seqs]
+  AttnSeq* seqs;     // [n_seqs]
+  AttnHdr* hdr;
+  AttnUnit* units;
+  AttnRec* recs;
+  float* part_o;     // [slot * Hkv + head][rows_slot][d]
+  float2* part_ml;   // [slot * Hkv + head][rows_slot]: maximum (log2 units) and sum
+  alignas(64) CUtensorMap map_q;
+  alignas(64) CUtensorMap map_k;
+  alignas(64) CUtensorMap map_v;
 };
 
 namespace {
 
-__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnArgs a) {
+// Key tiles that a block of np positions sees, the first of them `seen` keys.
+__device__ __forceinline__ int tiles_of(int seen, int np) {
+  const int last = seen + np - 1;
+  return last > 0 ? (last + kAttnTile - 1) / kAttnTile : 0;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constant__ AttnArgs a) {
   __shared__ int sh[32];
-  int seen = 0;
+  __shared__ int bins[kPlanThreads];
+  __shared__ unsigned long long s_work;
+  __shared__ int s_slots, s_recs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BP = 2 * a.PT;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (tid == 0) {
+    s_work = 0;
+    s_slots = s_recs = 0;
+  }
+  bins[tid] = 0;
+  int seen_off = 0;
   for (int base = 0; base < a.n_seqs; base += kPlanThreads) {
-    const int i = base + threadIdx.x;
+    const int i = base + tid;
     const bool in = i < a.n_seqs;
     const int r0 = in ? a.offsets[i] : 0, r1 = in ? a.offsets[i + 1] : 0;
-    const int before = block_excl_max(r0, seen, sh);
+    const int before = block_excl_max(r0, seen_off, sh);
     if (!in) continue;
     const int kv0 = a.kv_begin ? a.kv_begin[i] : r0, len = a.kv_begin ? a.kv_len[i] : r1 - r0;
     const bool ok = rows_ok(r0, r1, before, a.T) && kv0 >= 0 && len >= 0 && len <= a.max_kv && kv0 <= a.kv_rows &&
@@ -46,62 +119,628 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnArgs a) {
     a.seqs[i] = AttnSeq{r0, ok ? r1 - r0 : -1, kv0, len};
     if (!ok) atomicOr(&a.ctrl->err, kErrBadRange);
   }
-}
-
-// One warp per query row and head, a lane per d / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(256) k_attn_rows(const AttnArgs a) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(w / a.Hq), h = (int)(w - (long long)t * a.Hq), kh = h / (a.Hq / a.Hkv);
-  if (t >= a.T) return;
-  AttnSeq seq{};
-  bool found = false;
-  for (int base = 0; base < a.n_seqs && !found; base += 32) {
-    AttnSeq c{0, -1, 0, 0};
-    if (base + lane < a.n_seqs) c = a.seqs[base + lane];
-    const unsigned hit = __ballot_sync(0xffffffffu, c.n > 0 && t >= c.row0 && t < c.row0 + c.n);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      seq = AttnSeq{__shfl_sync(0xffffffffu, c.row0, src), __shfl_sync(0xffffffffu, c.n, src),
-                    __shfl_sync(0xffffffffu, c.kv0, src), __shfl_sync(0xffffffffu, c.len, src)};
-      found = true;
+  __syncthreads();
+  // the call's key tiles, summed over blocks and key heads
+  unsigned long long work = 0;
+  for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
+    const AttnSeq q = a.seqs[s];
+    for (int b = lane; b * BP < q.n; b += 32) work += tiles_of(q.len - q.n + b * BP + 1, min(BP, q.n - b * BP));
+  }
+  if (work) atomicAdd(&s_work, work * a.Hkv);
+  __syncthreads();
+  // Pieces of at most P tiles: with P >= work / kAttnFill the pieces of cut blocks number at
+  // most 2 work / P <= kAttnMaxSlots (a block of t > P tiles makes ceil(t / P) < 2 t / P).
+  // Little work (up to 16 tiles per SM) is cut into one piece per SM, more into two.
+  const unsigned long long fill = s_work <= 16ull * (kAttnFill / 2) ? kAttnFill / 2 : kAttnFill;
+  const int P = (int)min(max((unsigned long long)kAttnMinPiece, (s_work + fill - 1) / fill), 1ull << 24);
+  // two rounds over the blocks: count the units by size, then place them, longest first
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
+      const AttnSeq q = a.seqs[s];
+      for (int b = lane; b * BP < q.n; b += 32) {
+        const int np = min(BP, q.n - b * BP), seen = q.len - q.n + b * BP + 1, t = tiles_of(seen, np);
+        const int cut = (t + P - 1) / P;                      // pieces
+        const int len = cut > 1 ? (t + cut - 1) / cut : t;    // tiles of each but the last
+        const int pieces = cut > 1 ? (t + len - 1) / len : 1;
+        const int bin = kPlanThreads - 1 - (int)((long long)len * (kPlanThreads - 1) / P);
+        if (pass == 0) {
+          atomicAdd(&bins[bin], pieces);
+          continue;
+        }
+        const int at = atomicAdd(&bins[bin], pieces);
+        int slot = -1;
+        if (pieces > 1) {
+          slot = atomicAdd(&s_slots, pieces);
+          a.recs[atomicAdd(&s_recs, 1)] = AttnRec{q.row0 + b * BP, np, seen, slot, pieces};
+        }
+        for (int i = 0; i < pieces; ++i)
+          a.units[at + i] = AttnUnit{q.row0 + b * BP, np, q.kv0, q.len, seen, i * len, min(t, (i + 1) * len),
+                                     slot < 0 ? -1 : slot + i};
+      }
+    }
+    __syncthreads();
+    if (pass == 0) {
+      int total = 0;
+      const int first = block_excl_sum(bins[tid], total, sh);
+      bins[tid] = first;
+      if (tid == 0) a.hdr->n_units = total * a.Hkv;
+      __syncthreads();
     }
   }
-  if (!found) return;
-  const int seen = seq.len - seq.n + (t - seq.row0) + 1;
-  float q[EPL], o[EPL], m = -INFINITY, l = 0.f;
+  if (tid == 0) a.hdr->n_recs = s_recs;
+}
+
+// ---------------------------------------------------------------------------------------
+// The attention kernel
+// ---------------------------------------------------------------------------------------
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kAttnThreads = 12 * 32;  // three warpgroups (the last two warps only fill theirs)
+// Registers: launched with 168 a thread (384 x 168 = 64,512), redistributed to 216 for the two
+// softmax warpgroups (a row's 128 scores stay in registers) and 72 for the third:
+// 256 x 216 + 128 x 72 = 64,512.
+constexpr int kSoftRegs = 216, kRestRegs = 72;
+constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
+
+template <int D>
+struct AttnSmem {
+  static constexpr int kTile = kAttnTile * D * 2;          // bytes of a Q, K or V tile
+  static constexpr int kBox = kAttnTile * 64 * 2;          // 64 columns of it: one TMA box, 128-byte rows
+  static constexpr int kStages = D == 128 ? 5 : 8;         // K and V tiles in the ring
+  static constexpr int kBytes = (2 + kStages) * kTile + 1024;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 fadd2p(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+
+#define MOE_R32(r) \
+  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), \
+      "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), \
+      "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), \
+      "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+#define MOE_RW32(r) \
+  "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), \
+      "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), \
+      "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), \
+      "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+#define MOE_IN32(r) \
+  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), \
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), \
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), \
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+
+// 32 columns of this warp's 32 TMEM lanes (thread = lane).  The registers hold the values only
+// after tmem_ld_done on them.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : MOE_R32(r)
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for every load of this thread; the register operands keep uses of r behind it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MOE_RW32(r)::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      MOE_IN32(r)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (TMEM) += A (TMEM, bf16 pairs: 8 columns per 16 of K) * B (shared memory)
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// V as the B operand: N (the head's columns) runs along the 128-byte rows, K along the rows.
+// 128-byte swizzle; the next 64 columns are one box further (LBO), the next 8 rows 1024 bytes
+// (SBO); a k-step of 16 rows advances the start by 2048 bytes.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t box) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((box >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// kind::f16, D fp32, A and B bf16, M = 128; b_mn: B is N-major
+__device__ __forceinline__ uint32_t attn_idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Unit number of this CTA's it-th round: rounds alternate direction, so that the CTA with the
+// longest unit of one round gets the shortest of the next.
+__device__ __forceinline__ int unit_index(int it) {
+  return it * (int)gridDim.x + ((it & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+// What every role derives from a unit: per tile (A: 0, B: 1) its positions and key tiles.
+struct AttnWork {
+  AttnUnit u;
+  int np[2], nk[2], n;  // positions, key tiles of the piece; the larger of nk
+};
+__device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, int idx, int& head) {
+  AttnWork w;
+  const int e = idx / a.Hkv;
+  head = idx - e * a.Hkv;
+  w.u = a.units[e];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) {
-    q[e] = bf1(a.q[((size_t)t * a.Hq + h) * D + lane * EPL + e]) * a.scale;
-    o[e] = 0.f;
+  for (int x = 0; x < 2; ++x) {
+    w.np[x] = max(0, min(a.PT, w.u.npos - x * a.PT));
+    const int t = w.np[x] > 0 ? tiles_of(w.u.seen + x * a.PT, w.np[x]) : 0;
+    w.nk[x] = max(0, min(w.u.kt1, t) - w.u.kt0);
   }
-  for (int j = 0; j < seen; ++j) {
-    const size_t at = ((size_t)(seq.kv0 + j) * a.Hkv + kh) * D + lane * EPL;
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) x = fmaf(q[e], bf1(a.k[at + e]), x);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    const float mn = fmaxf(m, x), f = m == mn ? 1.f : expf(m - mn), p = x == mn ? 1.f : expf(x - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = fmaf(o[e], f, p * bf1(a.v[at + e]));
-    m = mn;
+  w.n = max(w.nk[0], w.nk[1]);
+  return w;
+}
+
+__device__ __forceinline__ bool soft_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int lane) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity) ? 1 : 0);
+  if (!ok && lane == 0) atomicOr(&c->err, kErrTimeout);
+  return ok;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant__ AttnArgs a) {
+  using L = AttnSmem<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2], p_full[2], o_done[2], o_free[2],
+      v_fix, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte tiles
+  const uint32_t ring = smem + 2 * L::kTile;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);  // one arrival per softmax warp
+      mbar_init(&o_done[x], 1);
+      mbar_init(&o_free[x], 4);
+    }
+    mbar_init(&q_free, 1);
+    mbar_init(&v_fix, 1);
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;  // columns: S of A 0.., S of B 128.., O of A 256.., O of B 384..
+  pdl_wait();                    // the units are the plan kernel's, every input earlier work's
+  const int n_units = a.hdr->n_units;
+
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------ softmax and results ------------------------------
+    const int x = warp >> 2;                       // tile
+    const int r = (warp & 3) * 32 + lane;          // row = TMEM lane
+    const int pos = r / a.G, sub = r - pos * a.G;  // position and head of the group
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
+    const bool neg = a.scale_log2 < 0.f;  // then the largest x is the smallest product: work on -S
+    const float sl = fabsf(a.scale_log2);
+    int n_s = 0;  // S tiles taken so far = products with P waited for (one each)
+    bool alive = true;
+    for (int it = 0; alive && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
+      int head;
+      const AttnWork w = attn_work(a, unit_index(it), head);
+      const int np = x ? w.np[1] : w.np[0], nk = x ? w.nk[1] : w.nk[0];
+      if (np == 0) continue;
+      const int seen_r = pos < np ? w.u.seen + x * a.PT + pos : 0;  // keys this row sees (a row in use or 0)
+      const int seen_0 = w.u.seen + x * a.PT;                            // the tile's first position
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nk; ++j, ++n_s) {
+        if (!soft_wait(&s_full[x], n_s & 1, a.ctrl, lane)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) a.out[((size_t)t * a.Hq + h) * D + lane * EPL + e] = f2bf(seen > 0 ? o[e] / l : 0.f);
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + c * 32, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_done(s[c]);
+        const int kt = w.u.kt0 + j;
+        if (neg) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c][i] ^= 0x80000000u;
+        }
+        if ((kt + 1) * kAttnTile > seen_0) {  // a key of the tile is hidden from some row
+          const int lim = seen_r - kt * kAttnTile;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= lim) s[c][i] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][i]));
+        }
+        const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+        if (j == 0) {
+          m = m_new;
+        } else {
+          const bool up = (m_new - m) * sl > kRescale;
+          if (__any_sync(0xffffffffu, up)) {
+            // O holds the sums over the tiles before: wait for the last of their products
+            if (!soft_wait(&o_done[x], (n_s - 1) & 1, a.ctrl, lane)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = up ? ex2((m - m_new) * sl) : 1.f;
+            if (up) m = m_new;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_async(t_o + c * 32, o);
+              tmem_ld_done(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(t_o + c * 32, o);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : -m * sl;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t* sv = &s[half * 2 + (i >> 4)][(i & 15) * 2];
+            const float2 e = ffma2(make_float2(__uint_as_float(sv[0]), __uint_as_float(sv[1])), make_float2(sl, sl),
+                                   make_float2(ms, ms));
+            const float2 pv = make_float2(ex2(e.x), ex2(e.y));
+            sum[i & 1] = fadd2p(sum[i & 1], pv);
+            p[i] = pack_bf16(pv.x, pv.y);
+          }
+          tmem_st32(t_s + half * 32, p);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st_done();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!alive) break;
+      // the end of the unit: this row's O
+      if (nk > 0) {
+        if (!soft_wait(&o_done[x], (n_s - 1) & 1, a.ctrl, lane)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const bool mine = pos < np;
+      const size_t brow = (size_t)(x * a.PT + pos) * a.G + sub;  // row within the block
+      const size_t prow = ((size_t)max(w.u.slot, 0) * a.Hkv + head) * a.rows_slot + brow;
+      const float inv = seen_r > 0 ? 1.0f / l : 0.f;
+      uint16_t* orow = a.out + ((size_t)(w.u.row + x * a.PT + pos) * a.Hq + (size_t)head * a.G + sub) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (nk > 0) {
+          tmem_ld32_async(t_o + c * 32, o);
+          tmem_ld_done(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (mine && w.u.slot >= 0) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                 __uint_as_float(o[4 * i + 3]));
+        } else if (mine) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = seen_r > 0 ? pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv)
+                                : 0u;
+            dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (mine && w.u.slot >= 0) a.part_ml[prow] = make_float2(m == -INFINITY ? m : m * sl, l);
+      if (nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[x]);
+      }
+    }
+    if (!alive) s_abort = 1;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+  }
+  if (warp == kMmaWarp) {
+    // ------------------------------ MMA issuer ------------------------------
+    if (lane == 0) {
+      const uint32_t id_s = attn_idesc(kAttnTile, false), id_o = attn_idesc(D, true);
+      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};  // phases used of q_full, p_full, o_free
+      int kv = 0;                                             // tiles taken from the ring
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !wait_or_flag(bar, parity, a.ctrl)) ok = false;
+        if (s_abort) ok = false;
+        return ok;
+      };
+      auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
+        const uint64_t da = umma_desc_sw128(smem + x * L::kTile), db = umma_desc_sw128(ring + slot * L::kTile);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)((k / 4) * (L::kBox >> 4) + (k % 4) * 2);
+          umma_f16(tmem + x * 128, da + step, db + step, id_s, k > 0);
+        }
+        umma_commit(&s_full[x]);
+      };
+      for (int it = 0; ok && unit_index(it) < n_units && !s_abort; ++it) {
+        int head;
+        const AttnWork w = attn_work(a, unit_index(it), head);
+        if (w.n == 0) continue;
+        if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (w.nk[x] > 0) {
+            if (!wait(&q_full[x], n_q[x]++ & 1)) break;
+            tc_fence_after();
+            issue_s(x, kv % NS);
+          }
+        if (!ok) break;
+        umma_commit(&kv_empty[kv % NS]);
+        if (w.n == 1) umma_commit(&q_free);
+        for (int j = 0; j < w.n && ok; ++j) {
+          const int cv = kv + 2 * j + 1, ck = cv + 1;
+          if (!wait(&kv_full[cv % NS], (cv / NS) & 1)) break;
+          bool have_k = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= w.nk[x]) continue;
+            if (!wait(&p_full[x], n_p[x]++ & 1)) break;
+            if (j == 0 && !wait(&o_free[x], (n_o[x]++ & 1) ^ 1)) break;
+            tc_fence_after();
+            const uint64_t db = umma_desc_mn(ring + (cv % NS) * L::kTile, L::kBox);
+#pragma unroll
+            for (int k = 0; k < kAttnTile / 16; ++k)
+              umma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + k * 8, db + (uint64_t)(k * (2048 >> 4)), id_o,
+                          j > 0 || k > 0);
+            umma_commit(&o_done[x]);
+            if (j + 1 < w.nk[x]) {
+              // in issue order behind the product that reads P where this S goes
+              if (!have_k && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
+              have_k = true;
+              tc_fence_after();
+              issue_s(x, ck % NS);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&kv_empty[cv % NS]);
+          if (j + 1 < w.n) umma_commit(&kv_empty[ck % NS]);
+          if (j + 2 == w.n) umma_commit(&q_free);
+        }
+        kv += 2 * w.n;
+      }
+      if (!ok) s_abort = 1;
+      umma_commit(&drain);  // every MMA of this thread has completed once it arrives
+      if (!mbar_wait(&drain, 0)) atomicOr(&a.ctrl->err, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp == kLoadWarp) {
+    // ------------------------------ TMA loads ------------------------------
+    int kv = 0, n_q[2] = {0, 0}, n_act = 0, n_fix = 0;
+    bool ok = true;
+    const uint32_t q_bytes = (uint32_t)a.PT * a.G * D * 2;
+    for (int it = 0; ok && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
+      int head;
+      const AttnWork w = attn_work(a, unit_index(it), head);
+      if (w.n == 0) continue;
+      if (!soft_wait(&q_free, (n_act++ & 1) ^ 1, a.ctrl, lane)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (w.nk[x] > 0) {
+          if (lane == 0) {
+            mbar_expect_tx(&q_full[x], q_bytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_3d(smem + x * L::kTile + c * L::kBox, &a.map_q, c * 64, head * a.G, w.u.row + x * a.PT, &q_full[x]);
+          }
+          ++n_q[x];
+        }
+      for (int j = 0; j < w.n && ok; ++j) {
+        const int row = (w.u.kt0 + j) * kAttnTile, left = w.u.len - row;  // keys of the sequence from here on
+        for (int v = 0; v < 2; ++v, ++kv) {
+          const int s = kv % NS;
+          if (!soft_wait(&kv_empty[s], ((kv / NS) & 1) ^ 1, a.ctrl, lane) || warp_aborted(&s_abort)) {
+            ok = false;
+            break;
+          }
+          const CUtensorMap* map = v ? &a.map_v : &a.map_k;
+          const uint32_t dst = ring + s * L::kTile;
+          // Rows behind the sequence's last key hold anything.  Their scores are masked, but a
+          // weight of 0 times an infinity or NaN in v is NaN: such rows of a value tile are
+          // cleared before the MMAs see it.
+          const bool fix = v && left < kAttnTile;
+          uint64_t* bar = fix ? &v_fix : &kv_full[s];
+          if (lane == 0) {
+            mbar_expect_tx(bar, L::kTile);
+            for (int c = 0; c < D / 64; ++c) tma_3d(dst + c * L::kBox, map, c * 64, head, w.u.kv0 + row, bar);
+          }
+          if (fix) {
+            if (!soft_wait(&v_fix, n_fix++ & 1, a.ctrl, lane)) {
+              ok = false;
+              break;
+            }
+            for (int c = 0; c < D / 64; ++c)
+              for (int o = left * 128 + lane * 16; o < L::kBox; o += 512)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + c * L::kBox + o), "r"(0) : "memory");
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[s]);
+          }
+        }
+      }
+    }
+    if (!ok) s_abort = 1;
+    // no copy may still be landing when the CTA leaves
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (n_q[x] && !mbar_wait(&q_full[x], (n_q[x] - 1) & 1)) atomicOr(&a.ctrl->err, kErrTimeout);
+      drain_ring(kv_full, NS, kv, a.ctrl);
+      if (n_fix && !mbar_wait(&v_fix, (n_fix - 1) & 1)) atomicOr(&a.ctrl->err, kErrTimeout);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// Joins the pieces of the cut blocks: a CTA per row of a block (grid-stride), its four warps
+// share the pieces, a lane has D / 32 columns.  The pieces are added in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a) {
+  constexpr int EPL = D / 32;
+  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  if ((int)blockIdx.x >= a.hdr->n_recs) return;
+  const AttnRec rec = a.recs[blockIdx.x];
+  const int rows = rec.npos * a.G;  // rows of one key head
+  for (int i = blockIdx.y; i < rows * a.Hkv; i += gridDim.y) {
+    const int head = i / rows, row = i - head * rows, pos = row / a.G, sub = row - pos * a.G;
+    float m = -INFINITY, l = 0.f, o[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int p = warp; p < rec.pieces; p += 4) {
+      const size_t prow = ((size_t)(rec.slot + p) * a.Hkv + head) * a.rows_slot + row;
+      const float2 ml = a.part_ml[prow];
+      float v[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = a.part_o[prow * D + lane * EPL + e];
+      if (ml.y == 0.f) continue;  // the row sees none of this piece's keys
+      const float mn = fmaxf(m, ml.x), b = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - b), g = ex2(ml.x - b);
+      m = mn;
+      l = l * f + ml.y * g;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = o[e] * f + v[e] * g;
+    }
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      const float mn = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), b = mn == -INFINITY ? 0.f : mn;
+      float sum = 0.f, r = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (s_l[w] == 0.f) continue;
+        const float g = ex2(s_m[w] - b);
+        sum += s_l[w] * g;
+        r += s_o[w][threadIdx.x] * g;
+      }
+      a.out[((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + threadIdx.x] =
+          f2bf(rec.seen + pos > 0 ? r / sum : 0.f);
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
-  k_attn_plan<<<1, kPlanThreads, 0, s>>>(a);
-  const int blocks = (int)(((long long)a.T * a.Hq + 7) / 8);
-  if (a.d == 64) k_attn_rows<64><<<blocks, 256, 0, s>>>(a);
-  else k_attn_rows<128><<<blocks, 256, 0, s>>>(a);
-  return cudaGetLastError();
+// The most blocks a call can have, and the most units (see k_attn_plan).
+static long long attn_max_blocks(int n_seqs, int T, int PT) { return (long long)T / (2 * PT) + std::min(n_seqs, T); }
+static bool attn_may_cut(int max_kv) { return max_kv > kAttnMinPiece * kAttnTile; }
+
+template <int D>
+static cudaError_t launch_attn_d(const AttnArgs& a, int n_sm, cudaStream_t s) {
+  const long long blocks = attn_max_blocks(a.n_seqs, a.T, a.PT);
+  const long long units = (blocks + (attn_may_cut(a.max_kv) ? kAttnMaxSlots : 0)) * a.Hkv;
+  cudaError_t e = launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_attn<D>, dim3((unsigned)std::min<long long>(n_sm, units)), dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
+  if (e != cudaSuccess || !attn_may_cut(a.max_kv)) return e;
+  const unsigned recs = (unsigned)std::min<long long>(blocks, kAttnMaxSlots / 2);
+  return launch_pdl(k_attn_join<D>, dim3(recs, (unsigned)std::min<long long>(64, (long long)a.rows_slot * a.Hkv)), dim3(128),
+                    0, s, a);
+}
+
+cudaError_t launch_attn(AttnArgs& a, const void* q, const void* k, const void* v, cudaStream_t s) {
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // [row, head, column]: boxes of 64 columns x the group's heads x PT positions, or one head x 128 keys
+  const auto map = [&](CUtensorMap* m, const void* base, int rows, int heads, int box_heads, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)heads * a.d * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if ((e = map(&a.map_q, q, a.T, a.Hq, a.G, a.PT)) != cudaSuccess) return e;
+  // without keys no unit has a key tile and the maps are not used
+  if (a.kv_rows > 0) {
+    if ((e = map(&a.map_k, k, a.kv_rows, a.Hkv, 1, kAttnTile)) != cudaSuccess) return e;
+    if ((e = map(&a.map_v, v, a.kv_rows, a.Hkv, 1, kAttnTile)) != cudaSuccess) return e;
+  }
+  return a.d == 64 ? launch_attn_d<64>(a, n_sm, s) : launch_attn_d<128>(a, n_sm, s);
 }
 
 moe_status set_error(moe_status s, const char* fmt, ...);
@@ -121,15 +760,20 @@ static moe_status check_attn(const moe_attn_shape* shape, int32_t n_seqs, int32_
   if (n_seqs < 1 || n_seqs > kMaxSeqs) return set_error(MOE_ERR_INVALID, "n_seqs must be 1..%d (got %d)", kMaxSeqs, n_seqs);
   if (T < 0) return set_error(MOE_ERR_INVALID, "T must be >= 0 (got %d)", T);
   if (max_kv < 0) return set_error(MOE_ERR_INVALID, "max_kv must be >= 0 (got %d)", max_kv);
-  if (((long long)T * Hq + 7) / 8 > 0x7fffffffLL) return set_error(MOE_ERR_INVALID, "T * n_q_heads too large");
+  if (attn_max_blocks(n_seqs, T, kAttnTile / (Hq / Hkv)) * Hkv > 1LL << 30)
+    return set_error(MOE_ERR_INVALID, "T * n_q_heads too large");
   return MOE_OK;
 }
 
 struct AttnLayout {
-  size_t ctrl, seqs, total;
+  size_t ctrl, seqs, hdr, units, recs, part_o, part_ml, total;
+  int PT, rows_slot;
 };
 static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, int max_kv) {
   AttnLayout W{};
+  const int G = shape->n_q_heads / shape->n_kv_heads;
+  W.PT = kAttnTile / G;
+  W.rows_slot = std::min(2 * W.PT, std::max(T, 1)) * G;
   size_t pos = 0;
   auto take = [&](size_t bytes) {
     const size_t at = (size_t)round_up((int64_t)pos, kAlign);
@@ -138,6 +782,15 @@ static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, in
   };
   W.ctrl = take(sizeof(Ctrl));
   W.seqs = take(sizeof(AttnSeq) * (size_t)n_seqs);
+  W.hdr = take(sizeof(AttnHdr));
+  const size_t blocks = (size_t)attn_max_blocks(n_seqs, T, W.PT);
+  // The pieces of cut blocks number at most kAttnMaxSlots over all key heads; a call whose keys
+  // fit one piece cuts nothing.
+  const size_t slots = attn_may_cut(max_kv) ? kAttnMaxSlots : 0;
+  W.units = take(sizeof(AttnUnit) * (blocks + slots));
+  W.recs = take(sizeof(AttnRec) * std::min(blocks, slots / 2));
+  W.part_o = take(sizeof(float) * slots * W.rows_slot * shape->d);
+  W.part_ml = take(sizeof(float2) * slots * W.rows_slot);
   W.total = (size_t)round_up((int64_t)pos, kAlign);
   return W;
 }
@@ -167,7 +820,7 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   if (!kv_begin && kv_rows < T) return set_error(MOE_ERR_INVALID, "kv_rows must be >= T without kv_begin (got %d < %d)", kv_rows, T);
   if (T > 0 && (!q || !out)) return set_error(MOE_ERR_INVALID, "q and out must be non-NULL");
   if (T > 0 && kv_rows > 0 && (!k || !v)) return set_error(MOE_ERR_INVALID, "k and v must be non-NULL");
-  if (!std::isfinite(scale)) return set_error(MOE_ERR_INVALID, "scale must be finite");
+  if (!std::isfinite(scale * 1.44269504088896340736f)) return set_error(MOE_ERR_INVALID, "scale must be finite");
   if (!ws) return set_error(MOE_ERR_INVALID, "ws is NULL");
   const uintptr_t all = (uintptr_t)q_offsets | (uintptr_t)kv_begin | (uintptr_t)kv_len | (uintptr_t)q | (uintptr_t)k |
                         (uintptr_t)v | (uintptr_t)out | (uintptr_t)ws;
@@ -176,10 +829,32 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   if (ws_bytes < W.total) return set_error(MOE_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, W.total);
   if (T == 0) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  AttnArgs a{n_seqs, T, shape->n_q_heads, shape->n_kv_heads, shape->d, max_kv, kv_rows, scale, q_offsets, kv_begin,
-             kv_len, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-             static_cast<uint16_t*>(out), reinterpret_cast<Ctrl*>(w + W.ctrl), reinterpret_cast<AttnSeq*>(w + W.seqs)};
-  const cudaError_t e = launch_attn(a, static_cast<cudaStream_t>(stream));
+  AttnArgs a{};
+  a.n_seqs = n_seqs;
+  a.T = T;
+  a.Hq = shape->n_q_heads;
+  a.Hkv = shape->n_kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.d = shape->d;
+  a.PT = W.PT;
+  a.max_kv = max_kv;
+  a.kv_rows = kv_rows;
+  a.rows_slot = W.rows_slot;
+  // A scale of 0 (every key seen counts the same) as one whose scores vanish next to each other:
+  // 0 times the mask's infinity would be NaN.
+  a.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.44269504088896340736f;
+  a.offsets = q_offsets;
+  a.kv_begin = kv_begin;
+  a.kv_len = kv_len;
+  a.out = static_cast<uint16_t*>(out);
+  a.ctrl = reinterpret_cast<Ctrl*>(w + W.ctrl);
+  a.seqs = reinterpret_cast<AttnSeq*>(w + W.seqs);
+  a.hdr = reinterpret_cast<AttnHdr*>(w + W.hdr);
+  a.units = reinterpret_cast<AttnUnit*>(w + W.units);
+  a.recs = reinterpret_cast<AttnRec*>(w + W.recs);
+  a.part_o = reinterpret_cast<float*>(w + W.part_o);
+  a.part_ml = reinterpret_cast<float2*>(w + W.part_ml);
+  const cudaError_t e = launch_attn(a, q, k, v, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return MOE_OK;
 }

@@ -41,7 +41,9 @@
 // drains and frees its TMEM.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "host.cuh"
 #include "sync.cuh"
+#include "tc.cuh"
 
 #include <cuda_bf16.h>
 
@@ -142,90 +144,6 @@ __device__ __forceinline__ uint32_t umma_idesc(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// K-major operand with 128-byte swizzle (rows of 64 bf16 = 128 bytes, 16-byte chunks XOR-ed
-// with the row's position in its 8-row group; the layout TMA writes with SWIZZLE_128B).  The
-// k-step of one MMA (16 elements = 32 bytes) advances the start address; 8-row groups are
-// 1024 bytes apart.  Tiles start on 1024-byte boundaries.
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;                         // LBO (unused for swizzled K-major)
-  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;  // SBO: next 8-row group
-  d |= (uint64_t)1 << 46;                         // descriptor version (sm_100)
-  d |= (uint64_t)2 << 61;                         // layout: 128-byte swizzle
-  return d;
-}
-
-// TMA loads into this CTA's shared memory, completing on an mbarrier (transaction bytes).
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                       uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 16 / 32 consecutive accumulator columns of this warp's 32 TMEM lanes (one row per thread)
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 // int8 codes -> bf16 on fp32 pairs: the code at bit position p becomes the exact float
 // q*2^p by OR-ing it into the mantissa of 2^23 and subtracting 2^23; multiplying by s*2^-p
 // (exact) then gives s*q, without integer-to-float instructions.  (bf16 has too few mantissa
@@ -289,51 +207,6 @@ __device__ __forceinline__ uint4 perm_octet(const uint4& v) {
 
 __device__ __forceinline__ int core_off(int row, int koct) {  // byte offset in a stage tile
   return (row >> 3) * kSBO + koct * 128 + (row & 7) * 16;
-}
-
-__device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, Ctrl* c) {
-  if (mbar_wait_suspend(bar, parity)) return true;
-  atomicOr(&c->err, kErrTimeout);
-  return false;
-}
-
-// The abort flag as the whole warp sees it (one value for all lanes, so that no lane
-// leaves a loop whose other lanes go on to a __syncwarp).
-__device__ __forceinline__ bool warp_aborted(const int* flag) {
-  return __any_sync(0xffffffffu, *reinterpret_cast<const volatile int*>(flag) != 0);
-}
-
-// Bounded wait that sleeps between tries (32 ns doubling to 256 ns), so that a warp waiting
-// for its next stage leaves the issue slots to the warps that are converting one.
-__device__ __forceinline__ bool mbar_wait_backoff(uint64_t* b, uint32_t parity) {
-  if (mbar_try_wait(b, parity)) return true;
-  const unsigned long long t0 = now_ns();
-  uint32_t ns = 32;
-  for (;;) {
-    __nanosleep(ns);
-    if (mbar_try_wait(b, parity)) return true;
-    if (now_ns() - t0 > kWaitNs) return false;
-    ns = ns < 256 ? 2 * ns : 256;
-  }
-}
-// Every lane of a warp waits, and all take the same branch afterwards (a lane whose wait
-// ran out would otherwise leave the others behind at the next __syncwarp).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int lane) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait_backoff(bar, parity) ? 1 : 0);
-  if (!ok && lane == 0) atomicOr(&c->err, kErrTimeout);
-  return ok;
-}
-
-// Wait (bounded) for the last stages a loader issued into a ring of n full barriers, so that
-// no copy is still landing when the CTA leaves.  Normally the consumers have already waited
-// for them and this returns at once; after an abort a phase may lack other arrivals, and
-// the bound (far beyond any copy's latency) ends the wait.
-__device__ __forceinline__ void drain_ring(uint64_t* full, int n, int issued, Ctrl* c) {
-  for (int q = issued > n ? issued - n : 0; q < issued; ++q)
-    if (!mbar_wait(&full[q % n], (uint32_t)((q / n) & 1))) {
-      atomicOr(&c->err, kErrTimeout);
-      return;
-    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1252,24 +1125,6 @@ __global__ void k_router_units(GemmUnit* units, int* n_units, int T, int E) {
   if (i == 0) *n_units = mt_n * nt;
 }
 
-// Launches a kernel as a programmatic dependent of the kernel before it on the stream: it may
-// start while that kernel finishes and waits for it (pdl_wait) before reading its results.
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl(void (*fn)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                              Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...);
-}
-
 template <int BITS, int MODE>
 cudaError_t launch_gemm(const GemmArgs& g, int n_sm, cudaStream_t s) {
   const GemmSmem P = gemm_smem<BITS, MODE>();
@@ -1280,33 +1135,6 @@ cudaError_t launch_gemm(const GemmArgs& g, int n_sm, cudaStream_t s) {
   return launch_pdl(fn, dim3(n_sm), dim3(kGemmThreads), P.total, s, g);
 }
 
-// ---- TMA descriptors (host) ----
-// The driver's encoder is looked up through the runtime, so the library does not link the
-// driver library itself (it loads on machines without a GPU driver).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled_fn() {
-  static EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (EncodeTiledFn) nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
-                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
-  const EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  const CUresult r = fn(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 // bf16 row-major [rows, cols] (row stride ld elements): boxes of 64 columns x box_rows rows,
 // 128-byte swizzle (the operand layout of the MMAs)
 cudaError_t map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
