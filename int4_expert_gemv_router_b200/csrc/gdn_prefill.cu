@@ -2,21 +2,83 @@
 //
 // Per sequence and value head, with the state S (d_v x d_k, fp32) and the notation of gdn.cu:
 //
-//     S_t = e^{g_t} S_{t-1} + beta_t (v_t - e^{g_t} S_{t-1} k^_t) k^_t^T,   o_t = S_t q^_t
+//     S_t = e^{g_t} S_{t-1} + w_t k^_t^T,  w_t = beta_t (v_t - e^{g_t} S_{t-1} k^_t),  o_t = S_t q^_t
 //
-// k_gdn_plan checks the sequences' row ranges.  k_gdn_recur takes the tokens one after another:
-// a warp owns rows of S in registers, as in the decode step.
+// Taken 64 tokens at a time (the chunk's tokens i, j; S the state before it; G_i = g_1 + .. + g_i
+// inside it; D_ij = e^{G_i - G_j}), the writes solve a unit lower triangular system:
+//
+//     (I + L) W = diag(beta) R,  L_ij = beta_i D_ij k^_i.k^_j (j < i),  R = V - diag(e^G) K^ S^T
+//     O  = diag(e^G) Q^ S^T + (D o Q^ K^^T)_{j <= i} W
+//     S' = e^{G_64} S + (diag(e^{G_64 - G}) W)^T K^
+//
+// L needs no state, so everything but the products with S is done for all chunks at once:
+//
+//   k_gdn_plan   one CTA: checks the row ranges, lists the chunks, orders the sequences longest
+//                first (they are the critical path)
+//   k_gdn_chunk  a CTA per chunk and key head: norms, K K^T and Q K^T on the tensor cores, the
+//                decays, T' = (I + L)^-1 diag(beta) by forward substitution and P = D o Q^ K^^T;
+//                leaves K, Q, T' and P in the operand layout of the next kernel
+//   k_gdn_scan   the sequential part, W = T' R.  A slab of 16 state rows (of one sequence and value
+//                head) belongs to d_k / 64 warps, 64 columns each, and stays in their registers as
+//                MMA accumulators from the first chunk to the last; rows never mix, so nothing else
+//                is shared but the sums S k over the columns (through shared memory, one exchange
+//                a chunk).  Everything is held transposed (S [d_v, d_k], R^T, W^T [d_v, token]): an
+//                accumulator is then the next product's A operand without moving a value.
+//
+// Precision.  The state is fp32 and has to stay so, but the tensor cores take 16-bit operands.
+// K is exact: its rows, scaled by powers of two to a norm of 2^10 .. 2^11, fit fp16 (bf16 has
+// fewer bits), and the norm's factor is applied in fp32.  S, R and W are split x = hi + lo into two
+// fp16 values after scaling each row by a power of two to its largest element: 22 bits of the row's
+// size; T' likewise by its rows.  S K^T and W K take two products (hi, lo), T' R three (lo lo is
+// below 2^-22).  What only the bf16 output sees (Q S, P W) takes hi alone, 2^-12 of each weight.
+// mma.sync carries this, not tcgen05: the slab's products are 16 rows high, 8 to 64 wide and
+// dependent on each other, and a chunk's chain of six of them through TMEM (a round trip of
+// registers, TMEM, MMA and back for each) costs more than the products themselves.
 #include "../../include/moe.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "kernels.cuh"
 #include "seqs.cuh"
 #include "sync.cuh"
 
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
 namespace moe {
 
+constexpr int kGdnChunk = 64;     // tokens of a chunk
+constexpr int kGdnSlab = 16;      // state rows of a slab
+constexpr int kGdnSlice = 64;     // state columns of a warp
+
 struct GdnSeq {
-  int row0, n;  // first row and tokens; n < 0: left out
+  int row0, n;   // first row and tokens; n < 0: left out
+  int chunk0;    // its first chunk
 };
+struct GdnChunk {
+  int row0, n;
+};
+struct GdnHdr {
+  int n_chunks;
+};
+
+// What k_gdn_chunk leaves for one chunk and value head.  T' and P as B operands of
+// mma.m16n8k16 (n = token i in tiles of 8, k = token j in steps of 16): the 20 (tile, step)
+// blocks of the lower triangle, a lane's registers together.
+struct GdnTP {
+  static constexpr int kBlocks = 20;
+  uint4 t[kBlocks][32];              // T': hi (2 registers), lo (2 registers)
+  uint2 p[kBlocks][32];              // P
+  float xa[kGdnChunk];               // -e^{G_i} / |k_i|: what the state recalls, in R
+  float oa[kGdnChunk];               // e^{G_i} / (|q_i| sqrt(d_k))
+  float wd[kGdnChunk];               // e^{G_64 - G_i} / |k_i|
+  float ts[kGdnChunk], ps[kGdnChunk];  // scales of the rows of T' and P
+  float keep[32];                    // [0]: e^{G_64}
+};
+static_assert(sizeof(GdnTP) % 128 == 0, "bulk copies and alignment");
+// Block of token tile t (8 tokens) and step k (16 tokens), k <= t / 2
+__host__ __device__ constexpr int gdn_block(int t, int k) { return (t / 2) * (t / 2 + 1) + (t & 1) * (t / 2 + 1) + k; }
+static_assert(gdn_block(7, 3) == GdnTP::kBlocks - 1, "lower triangle");
 
 struct GdnPrefillArgs {
   int n_seqs, T, Hk, Hv, dk, dv;
@@ -29,104 +91,736 @@ struct GdnPrefillArgs {
   const float* g;        // [T, Hv]
   const float* beta;     // [T, Hv]
   uint16_t* out;         // bf16 [T, Hv, dv]
+  int slabs;             // slabs of a scan CTA
   Ctrl* ctrl;
+  GdnHdr* hdr;
   GdnSeq* seqs;          // [n_seqs]
+  int32_t* order;        // [n_seqs] sequences, longest first
+  GdnChunk* chunks;
+  uint8_t* img;          // [chunk][Hk]: fp16 K then Q, 64 x dk each, rows' 16-byte pieces XORed with row & 7
+  GdnTP* tp;             // [chunk][Hv]
 };
 
 namespace {
 
 __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs a) {
   __shared__ int sh[32];
-  int seen = 0;
+  __shared__ int bins[kPlanThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  bins[tid] = 0;
+  int seen = 0, chunks = 0;
   for (int base = 0; base < a.n_seqs; base += kPlanThreads) {
-    const int i = base + threadIdx.x;
+    const int i = base + tid;
     const bool in = i < a.n_seqs;
     const int r0 = in ? a.offsets[i] : 0, r1 = in ? a.offsets[i + 1] : 0;
     const int before = block_excl_max(r0, seen, sh);
+    const bool ok = in && rows_ok(r0, r1, before, a.T);
+    const int nc = ok ? (r1 - r0 + kGdnChunk - 1) / kGdnChunk : 0;
+    const int c0 = block_excl_sum(nc, chunks, sh);
     if (!in) continue;
-    const bool ok = rows_ok(r0, r1, before, a.T);
-    a.seqs[i] = GdnSeq{r0, ok ? r1 - r0 : -1};
+    a.seqs[i] = GdnSeq{r0, ok ? r1 - r0 : -1, c0};
     if (!ok) atomicOr(&a.ctrl->err, kErrBadRange);
+  }
+  if (tid == 0) a.hdr->n_chunks = chunks;
+  __syncthreads();
+  for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
+    const GdnSeq q = a.seqs[s];
+    for (int c = lane; c * kGdnChunk < q.n; c += 32)
+      a.chunks[q.chunk0 + c] = GdnChunk{q.row0 + c * kGdnChunk, min(kGdnChunk, q.n - c * kGdnChunk)};
+  }
+  // sequences by length, longest first, in kPlanThreads classes
+  const int per = a.T / (kPlanThreads - 1) + 1;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int s = tid; s < a.n_seqs; s += kPlanThreads) {
+      const int bin = kPlanThreads - 1 - max(0, a.seqs[s].n) / per;
+      const int at = atomicAdd(&bins[bin], 1);
+      if (pass) a.order[at] = s;
+    }
+    __syncthreads();
+    if (!pass) {
+      int total = 0;
+      const int first = block_excl_sum(bins[tid], total, sh);
+      bins[tid] = first;
+      __syncthreads();
+    }
   }
 }
 
-constexpr int kRecurWarps = 8, kRecurRpw = 4, kRecurRows = kRecurWarps * kRecurRpw;
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d (16 x 8, fp32) += a (16 x 16, fp16) b (16 x 8, fp16).  With g = lane / 4, u = 2 (lane % 4):
+// d0,d1 = (g, u..u+1), d2,d3 = (g + 8, u..); a0 = (g, u..), a1 = (g + 8, u..), a2 = (g, u + 8..),
+// a3 = (g + 8, u + 8..); b0 = (k u.., n g), b1 = (k u + 8.., n g).
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
-__device__ __forceinline__ float lanes_sum(float v) {
+// The power of two that brings a row whose largest element is m to [2^14, 2^15) (exact; rows of
+// zeros and of values below 2^-112 by 2^126), and its inverse.
+__device__ __forceinline__ void row_scale(float m, float& up, float& down) {
+  const int e = max((int)(__float_as_uint(m) >> 23) - 127 - 14, -126);
+  up = __uint_as_float((uint32_t)(127 - e) << 23);
+  down = __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// Accumulators of N tiles of 8 columns (rows g and g + 8 of a slab) -> the largest element of
+// each of the two rows over the warp's columns.
+template <int N>
+__device__ __forceinline__ void row_max(const float (&v)[N][4], float& m0, float& m1) {
+  m0 = m1 = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int t = 0; t < N; ++t) {
+    m0 = fmaxf(m0, fmaxf(fabsf(v[t][0]), fabsf(v[t][1])));
+    m1 = fmaxf(m1, fmaxf(fabsf(v[t][2]), fabsf(v[t][3])));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+}
+// hi + lo of the scaled rows, as A operands: registers (2t, 2t + 1) of the two tiles of a step of 16
+template <int N>
+__device__ __forceinline__ void split(const float (&v)[N][4], float up0, float up1, uint32_t (&hi)[N][2], uint32_t (&lo)[N][2]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const float x0 = v[t][0] * up0, x1 = v[t][1] * up0, x2 = v[t][2] * up1, x3 = v[t][3] * up1;
+    hi[t][0] = pack_h2(x0, x1);
+    hi[t][1] = pack_h2(x2, x3);
+    const float2 h0 = unpack_h2(hi[t][0]), h1 = unpack_h2(hi[t][1]);
+    lo[t][0] = pack_h2(x0 - h0.x, x1 - h0.y);
+    lo[t][1] = pack_h2(x2 - h1.x, x3 - h1.y);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// k_gdn_chunk
+// ---------------------------------------------------------------------------------------
+constexpr int kChunkThreads = 128;  // two warps per value head, two value heads at a time
+constexpr int kMatLd = 68;          // row stride (floats) of the 64 x 64 matrices: 16-byte rows
+
+template <int DK>
+struct GdnChunkSmem {
+  static constexpr int kImg = kGdnChunk * DK * 2;
+  static constexpr int kMat = kGdnChunk * kMatLd * 4;
+  static constexpr int kBytes = 2 * kImg + 4 * kMat;  // K, Q; K K^T, Q K^T; L (then T') of two heads
+};
+
+// Column j of (I + L)^-1 for the rows LO .. 63 (j >= LO): t_i = [i = j] - sum_{LO <= m < i} L_im t_m.
+template <int LO>
+__device__ __forceinline__ void solve_column(const float* L, int j, float (&t)[kGdnChunk - LO]) {
+#pragma unroll
+  for (int i = LO; i < kGdnChunk; ++i) {
+    float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+    for (int m = LO; m < i; m += 4) {
+      const float4 l = *reinterpret_cast<const float4*>(L + i * kMatLd + m);
+      s0 = fmaf(-l.x, t[m - LO], s0);
+      if (m + 1 < i) s1 = fmaf(-l.y, t[m + 1 - LO], s1);
+      if (m + 2 < i) s0 = fmaf(-l.z, t[m + 2 - LO], s0);
+      if (m + 3 < i) s1 = fmaf(-l.w, t[m + 3 - LO], s1);
+    }
+    t[i - LO] = s0 + s1;
+  }
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kRecurWarps * 32) k_gdn_recur(const GdnPrefillArgs a) {
+__global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArgs a) {
+  using M = GdnChunkSmem<DK>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk], s_ts[2][kGdnChunk];
+  __shared__ double s_G[2][kGdnChunk], s_low[2][kGdnChunk];  // G_i and the least G_j up to i
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int chunk = blockIdx.x / a.Hk, kh = blockIdx.x - chunk * a.Hk;
+  if (chunk >= a.hdr->n_chunks) return;
+  const GdnChunk C = a.chunks[chunk];
+  uint8_t* img[2] = {smem, smem + M::kImg};
+  float* kk = reinterpret_cast<float*>(smem + 2 * M::kImg);
+  float* qk = kk + kGdnChunk * kMatLd;
+  float* Lh = qk + kGdnChunk * kMatLd;
+
+  // K and Q: rows scaled to a norm in [2^10, 2^11), as fp16
   constexpr int EPL = DK / 32;
-  const int blocks = (a.dv + kRecurRows - 1) / kRecurRows;
-  const int bh = blockIdx.x / blocks, rb = blockIdx.x - bh * blocks;
-  const int s = bh / a.Hv, h = bh - s * a.Hv, kh = h / (a.Hv / a.Hk);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const GdnSeq seq = a.seqs[s];
-  if (seq.n < 0) return;
-  const int i0 = rb * kRecurRows + warp * kRecurRpw;
-  float row[kRecurRpw][EPL];
+  for (int r = warp; r < 2 * kGdnChunk; r += kChunkThreads / 32) {
+    const int z = r >> 6, row = r & 63;
+    float x[EPL], ss = 0.f;
+    const uint16_t* src = (z ? a.q : a.k) + ((size_t)(C.row0 + row) * a.Hk + kh) * DK + lane * EPL;
 #pragma unroll
-  for (int r = 0; r < kRecurRpw; ++r)
-#pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      row[r][e] = a.S_in && i0 + r < a.dv ? a.S_in[((size_t)bh * a.dv + i0 + r) * DK + lane * EPL + e] : 0.f;
-  for (int t = seq.row0; t < seq.row0 + seq.n; ++t) {
-    float kn[EPL], qn[EPL], kk = 0.f, qq = 0.f;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      kn[e] = bf1(a.k[((size_t)t * a.Hk + kh) * DK + lane * EPL + e]);
-      qn[e] = bf1(a.q[((size_t)t * a.Hk + kh) * DK + lane * EPL + e]);
-      kk = fmaf(kn[e], kn[e], kk);
-      qq = fmaf(qn[e], qn[e], qq);
+    for (int e = 0; e < EPL; e += 2) {
+      const uint32_t w = row < C.n ? *reinterpret_cast<const uint32_t*>(src + e) : 0u;
+      x[e] = bf_lo(w);
+      x[e + 1] = bf_hi(w);
+      ss = fmaf(x[e], x[e], fmaf(x[e + 1], x[e + 1], ss));
     }
-    const float ki = 1.0f / fmaxf(sqrtf(lanes_sum(kk)), 1e-6f);
-    const float qi = 1.0f / fmaxf(sqrtf(lanes_sum(qq)), 1e-6f) * rsqrtf((float)DK);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      kn[e] *= ki;
-      qn[e] *= qi;
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float norm = sqrtf(ss);
+    // 2^e2 brings the norm to [2^10, 2^11).  A row of a norm below 2^-100 (it vanishes next to
+    // 1e-6), and one whose sum of squares overflows (1 / inf), is 0; infinities and NaN give NaN.
+    const int ne = (int)(__float_as_uint(norm) >> 23) - 127;
+    const bool zero = ne <= -100 || ne == 128;
+    const float up = zero ? 0.f : __uint_as_float((uint32_t)(137 - ne) << 23);
+    const float down = zero ? 0.f : __uint_as_float((uint32_t)(117 + ne) << 23);
+    if (lane == 0) {
+      const float c = zero ? 0.f : down / fmaxf(norm, 1e-6f);  // the normalised row is c times the stored one
+      if (z) s_cq[row] = c * rsqrtf((float)DK);
+      else s_ck[row] = c;
     }
-    const float alpha = expf(a.g[(size_t)t * a.Hv + h]), beta = a.beta[(size_t)t * a.Hv + h];
+    uint32_t h[EPL / 2];
 #pragma unroll
-    for (int r = 0; r < kRecurRpw; ++r) {
-      if (i0 + r >= a.dv) continue;  // the whole warp takes the same branch
-      const size_t at = ((size_t)t * a.Hv + h) * a.dv + i0 + r;
-      float u = 0.f, o = 0.f;
+    for (int e = 0; e < EPL; e += 2) h[e / 2] = pack_h2(x[e] * up, x[e + 1] * up);
+    const int col = lane * EPL;  // 16-byte piece col / 8
+    uint8_t* dst = img[z] + row * DK * 2 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
+    if constexpr (EPL == 2) *reinterpret_cast<uint32_t*>(dst) = h[0];
+    else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  __syncthreads();
+  {
+    const uint4* src = reinterpret_cast<const uint4*>(smem);
+    uint4* dst = reinterpret_cast<uint4*>(a.img + ((size_t)chunk * a.Hk + kh) * 2 * M::kImg);
+    for (int i = tid; i < 2 * M::kImg / 16; i += kChunkThreads) dst[i] = src[i];
+  }
+  // K K^T and Q K^T, lower triangle: rows in tiles of 16 (A), columns in pairs of tiles of 8 (B)
+  for (int w = warp; w < 20; w += kChunkThreads / 32) {
+    const int z = w / 10, u = w % 10;  // u: (row tile i, column pair j <= i)
+    const int i = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, j = u - i * (i + 1) / 2;
+    const uint32_t sa = smem_u32(img[z]), sb = smem_u32(img[0]);
+    const int ra = i * 16 + (lane & 15), rb = j * 16 + (lane & 7) + ((lane >> 4) << 3);
+    float d[2][4] = {};
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) u = fmaf(row[r][e], kn[e], u);
-      u = lanes_sum(u);
-      const float c = beta * (bf1(a.v[at]) - alpha * u);
+    for (int k = 0; k < DK / 16; ++k) {
+      uint32_t A[4], B[4];
+      ldsm4(sa + ra * DK * 2 + (((2 * k + (lane >> 4)) ^ (ra & 7)) << 4), A);
+      ldsm4(sb + rb * DK * 2 + (((2 * k + ((lane >> 3) & 1)) ^ (rb & 7)) << 4), B);
+      mma16(d[0], A[0], A[1], A[2], A[3], B[0], B[1]);
+      mma16(d[1], A[0], A[1], A[2], A[3], B[2], B[3]);
+    }
+    float* dst = z ? qk : kk;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        row[r][e] = fmaf(alpha, row[r][e], c * kn[e]);
-        o = fmaf(row[r][e], qn[e], o);
-      }
-      o = lanes_sum(o);
-      if (lane == 0) a.out[at] = f2bf(o);
+    for (int t = 0; t < 2; ++t) {
+      const int r = i * 16 + (lane >> 2), c = j * 16 + t * 8 + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(dst + r * kMatLd + c) = make_float2(d[t][0], d[t][1]);
+      *reinterpret_cast<float2*>(dst + (r + 8) * kMatLd + c) = make_float2(d[t][2], d[t][3]);
     }
   }
+  const int rep = a.Hv / a.Hk, pair = warp >> 1, j = tid & 63;
+  float* L = Lh + pair * kGdnChunk * kMatLd;
+  for (int h0 = 0; h0 < rep; h0 += 2) {
+    const bool on = h0 + pair < rep;
+    const int h = kh * rep + h0 + pair;
+    // G in 64 bits: differences of sums that may be large (a forgotten state's g is clamped: e^-1e4 = 0)
+    if (on && (warp & 1) == 0) {
+      double x[2];
 #pragma unroll
-  for (int r = 0; r < kRecurRpw; ++r)
-    if (i0 + r < a.dv)
+      for (int e = 0; e < 2; ++e) {
+        const int t = 2 * lane + e;
+        const float gt = t < C.n ? a.g[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+        x[e] = gt < -1e4f ? -1e4 : (double)gt;
+        s_beta[pair][t] = t < C.n ? a.beta[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+      }
+      double sum = x[0] + x[1];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) a.S_out[((size_t)bh * a.dv + i0 + r) * DK + lane * EPL + e] = row[r][e];
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+      const double g1 = sum, g0 = sum - x[1];
+      double low = fmin(g0, g1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, low, o);
+        if (lane >= o) low = fmin(low, u);
+      }
+      double before = __shfl_up_sync(0xffffffffu, low, 1);
+      s_G[pair][2 * lane] = g0;
+      s_G[pair][2 * lane + 1] = g1;
+      s_low[pair][2 * lane] = lane ? fmin(before, g0) : g0;
+      s_low[pair][2 * lane + 1] = low;
+    }
+    __syncthreads();
+    if (on) {  // thread j: column j of L
+      const double Gj = s_G[pair][j];
+      const float cj = s_ck[j];
+      for (int i = 0; i < kGdnChunk; ++i) {
+        float l = 0.f;
+        if (i > j) l = s_beta[pair][i] * expf((float)(s_G[pair][i] - Gj)) * (s_ck[i] * cj) * kk[i * kMatLd + j];
+        L[i * kMatLd + j] = l;
+      }
+    }
+    __syncthreads();
+    float t[kGdnChunk];
+    if (on) {
+      if (j < 32) {
+        solve_column<0>(L, j, t);
+      } else {
+        float u[32];
+        solve_column<32>(L, j, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          t[i] = 0.f;
+          t[32 + i] = u[i];
+        }
+      }
+    }
+    __syncthreads();
+    if (on) {
+      const float bj = s_beta[pair][j];
+#pragma unroll
+      for (int i = 0; i < kGdnChunk; ++i) L[i * kMatLd + j] = t[i] * bj;
+    }
+    __syncthreads();
+    GdnTP* tp = a.tp + (size_t)chunk * a.Hv + h;
+    if (on) {  // thread j: row j's scale and factors
+      float m = 0.f;
+      for (int c = 0; c <= j; ++c) m = fmaxf(m, fabsf(L[j * kMatLd + c]));
+      float up, down;
+      row_scale(m, up, down);
+      s_ts[pair][j] = up;
+      const double G = s_G[pair][j], last = s_G[pair][kGdnChunk - 1];
+      const float eg = expf((float)G);
+      tp->ts[j] = down;
+      // P is held relative to its row's least decayed entry and times 2^10 (fp16's range)
+      tp->ps[j] = expf((float)(G - s_low[pair][j])) * 0x1p-10f;
+      tp->xa[j] = -eg * s_ck[j];
+      tp->oa[j] = eg * s_cq[j];
+      tp->wd[j] = expf((float)(last - G)) * s_ck[j];
+      if (j < 32) tp->keep[j] = expf((float)last);
+    }
+    __syncthreads();
+    if (on) {
+      for (int x = (warp & 1); x < GdnTP::kBlocks; x += 2) {
+        // block x: token tile tt, step ks
+        const int half = x < 2 ? 0 : x < 6 ? 1 : x < 12 ? 2 : 3;
+        const int rest = x - half * (half + 1), tt = 2 * half + rest / (half + 1), ks = rest % (half + 1);
+        const int i = tt * 8 + (lane >> 2), c0 = ks * 16 + 2 * (lane & 3);
+        const float up = s_ts[pair][i];
+        const double low = s_low[pair][i];
+        const float cq = s_cq[i] * 1024.f;
+        float tv[4], pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = c0 + (e & 1) + (e >> 1) * 8;
+          tv[e] = c <= i ? L[i * kMatLd + c] * up : 0.f;
+          pv[e] = c <= i ? expf((float)(low - s_G[pair][c])) * (cq * s_ck[c]) * qk[i * kMatLd + c] : 0.f;
+        }
+        uint4 o;
+        o.x = pack_h2(tv[0], tv[1]);
+        o.y = pack_h2(tv[2], tv[3]);
+        const float2 f0 = unpack_h2(o.x), f1 = unpack_h2(o.y);
+        o.z = pack_h2(tv[0] - f0.x, tv[1] - f0.y);
+        o.w = pack_h2(tv[2] - f1.x, tv[3] - f1.y);
+        tp->t[x][lane] = o;
+        tp->p[x][lane] = make_uint2(pack_h2(pv[0], pv[1]), pack_h2(pv[2], pv[3]));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// k_gdn_scan
+// ---------------------------------------------------------------------------------------
+template <int DK>
+struct GdnScanSmem {
+  static constexpr int kWarps = DK / kGdnSlice;             // warps of a slab
+  static constexpr int kImg = kGdnChunk * DK * 2;
+  static constexpr int kTp = 2 * kImg;                      // stage: K, Q, T' and P, V
+  static constexpr int kV = kTp + (int)sizeof(GdnTP);
+  static constexpr int kVSlab = kGdnChunk * kGdnSlab * 2;   // 32-byte rows, 16-byte pieces XORed with bit 2 of the row
+  static constexpr int stage(int slabs) { return kV + slabs * kVSlab; }
+  // exchange: per slab and warp, 8 tiles of S k and 8 of S q
+  static constexpr int kXch = kWarps > 1 ? kWarps * 16 * 512 : 0;
+  static constexpr int bytes(int slabs) { return 2 * stage(slabs) + slabs * kXch; }
+};
+
+__device__ __forceinline__ void slab_sync(int slab, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(slab + 1), "r"(threads) : "memory");
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
+  using M = GdnScanSmem<DK>;
+  constexpr int NW = M::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slab = warp / NW, w = warp - slab * NW;
+  const int g = lane >> 2, u = 2 * (lane & 3);
+  const int stage_bytes = M::stage(a.slabs);
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1 + blockDim.x);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  const int blocks = (a.dv + kGdnSlab * a.slabs - 1) / (kGdnSlab * a.slabs);
+  const int per = a.Hv * blocks;
+  const int s = a.order[blockIdx.x / per], rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
+  const int kh = h / (a.Hv / a.Hk);
+  const GdnSeq seq = a.seqs[s];
+  if (seq.n < 0) return;
+  const int n_ch = (seq.n + kGdnChunk - 1) / kGdnChunk;
+  const int v0 = rb * a.slabs * kGdnSlab;       // first state row of the CTA
+  const int vr = v0 + slab * kGdnSlab + g;      // this lane's rows: vr and vr + 8
+  const size_t state = (size_t)s * a.Hv + h;
+  float* So = a.S_out + state * a.dv * DK;
+
+  float S[8][4];  // tiles of 8 columns of this warp's 64
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float2 x = make_float2(0.f, 0.f);
+      if (a.S_in && vr + 8 * e < a.dv)
+        x = *reinterpret_cast<const float2*>(a.S_in + (state * a.dv + vr + 8 * e) * DK + w * kGdnSlice + t * 8 + u);
+      S[t][2 * e] = x.x;
+      S[t][2 * e + 1] = x.y;
+    }
+
+  const bool v_wide = a.dv % 8 == 0;
+  auto load = [&](int c) {  // chunk c into its stage; every thread arrives on the stage's barrier
+    uint8_t* st = smem + (c & 1) * stage_bytes;
+    const size_t ch = (size_t)seq.chunk0 + c;
+    if (tid == 0) {
+      mbar_expect_tx(&full[c & 1], M::kV);
+      bulk_g2s(st, a.img + (ch * a.Hk + kh) * 2 * M::kImg, 2 * M::kImg, &full[c & 1]);
+      bulk_g2s(st + M::kTp, a.tp + ch * a.Hv + h, sizeof(GdnTP), &full[c & 1]);
+    }
+    const int row0 = seq.row0 + c * kGdnChunk, n = min(kGdnChunk, seq.n - c * kGdnChunk);
+    // V: per slab, token and half (8 values)
+    for (int i = tid; i < a.slabs * kGdnChunk * 2; i += blockDim.x) {
+      const int half = i % (2 * a.slabs), r = i / (2 * a.slabs), col = v0 + half * 8;
+      uint8_t* dst = st + M::kV + (half >> 1) * M::kVSlab + r * 32 + (((half & 1) ^ ((r >> 2) & 1)) << 4);
+      const uint16_t* src = a.v + ((size_t)(row0 + r) * a.Hv + h) * a.dv + col;
+      if (v_wide && r < n && col < a.dv) {
+        cp_async16(dst, src);
+      } else {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t l0 = r < n && col + 2 * e < a.dv ? src[2 * e] : 0, l1 = r < n && col + 2 * e + 1 < a.dv ? src[2 * e + 1] : 0;
+          x[e] = l0 | (l1 << 16);
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    cp_async_arrive(&full[c & 1]);
+  };
+
+  bool ok = true;
+  int issued = 0;
+  if (n_ch > 0) load(issued++);
+  for (int c = 0; c < n_ch; ++c) {
+    // everyone is done with the other stage and with the exchange area (and the plain stores of
+    // this chunk's V are visible)
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    if (c + 1 < n_ch) load(issued++);
+    ok = mbar_wait(&full[c & 1], (c >> 1) & 1);
+    const uint32_t st = smem_u32(smem) + (c & 1) * stage_bytes;
+    const uint32_t sK = st, sQ = st + M::kImg;
+    const GdnTP* tp = reinterpret_cast<const GdnTP*>(smem + (c & 1) * stage_bytes + M::kTp);
+
+    // ---- X^T = S K^T (hi, lo) and Y^T = S Q^T (hi), over this warp's columns ----
+    float X[8][4], Y[8][4];
+    {
+      float m0, m1, up0, up1, dn0, dn1;
+      row_max(S, m0, m1);
+      row_scale(m0, up0, dn0);
+      row_scale(m1, up1, dn1);
+      uint32_t hi[8][2], lo[8][2];
+      split(S, up0, up1, hi, lo);
+#pragma unroll
+      for (int tg = 0; tg < 8; tg += 4) {
+        uint32_t B[4][8];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // K, then Q
+          float (&D)[8][4] = z ? Y : X;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int row = (tg + t) * 8 + (lane & 7);
+            const uint32_t base = (z ? sQ : sK) + row * DK * 2;
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+              uint32_t r[4];
+              ldsm4(base + (((w * 8 + k2 * 4 + (lane >> 3)) ^ (row & 7)) << 4), r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) B[t][k2 * 4 + e] = r[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) D[tg + t][e] = 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              mma16(D[tg + t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], B[t][2 * k], B[t][2 * k + 1]);
+            if (!z) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                mma16(D[tg + t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], B[t][2 * k], B[t][2 * k + 1]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        X[t][0] *= dn0;
+        X[t][1] *= dn0;
+        X[t][2] *= dn1;
+        X[t][3] *= dn1;
+        Y[t][0] *= dn0;
+        Y[t][1] *= dn0;
+        Y[t][2] *= dn1;
+        Y[t][3] *= dn1;
+      }
+    }
+    // ---- sums over the slab's warps (each the same, in the same order); of Y only the tiles
+    // t % NW == w that this warp finishes ----
+    if constexpr (NW > 1) {
+      float4* xch = reinterpret_cast<float4*>(smem + 2 * stage_bytes + slab * M::kXch);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        xch[(w * 16 + t) * 32 + lane] = make_float4(X[t][0], X[t][1], X[t][2], X[t][3]);
+        if (t % NW != w) xch[(w * 16 + 8 + t) * 32 + lane] = make_float4(Y[t][0], Y[t][1], Y[t][2], Y[t][3]);
+      }
+      slab_sync(slab, NW * 32);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float4 sx = make_float4(0.f, 0.f, 0.f, 0.f), sy = sx;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) {
+          const float4 x = v == w ? make_float4(X[t][0], X[t][1], X[t][2], X[t][3]) : xch[(v * 16 + t) * 32 + lane];
+          sx = make_float4(sx.x + x.x, sx.y + x.y, sx.z + x.z, sx.w + x.w);
+          if (t % NW == w) {
+            const float4 y = v == w ? make_float4(Y[t][0], Y[t][1], Y[t][2], Y[t][3]) : xch[(v * 16 + 8 + t) * 32 + lane];
+            sy = make_float4(sy.x + y.x, sy.y + y.y, sy.z + y.z, sy.w + y.w);
+          }
+        }
+        X[t][0] = sx.x;
+        X[t][1] = sx.y;
+        X[t][2] = sx.z;
+        X[t][3] = sx.w;
+        if (t % NW == w) {
+          Y[t][0] = sy.x;
+          Y[t][1] = sy.y;
+          Y[t][2] = sy.z;
+          Y[t][3] = sy.w;
+        }
+      }
+    }
+    // ---- R^T = V^T - e^G S k ----
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) {
+      uint32_t r[4];  // (tile t, rows g), (t, g + 8), (t + 1, g), (t + 1, g + 8)
+      const int row = (t + (lane >> 4)) * 8 + (lane & 7), half = (lane >> 3) & 1;
+      ldsm4_t(st + M::kV + slab * M::kVSlab + row * 32 + ((half ^ ((row >> 2) & 1)) << 4), r);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 xa = *reinterpret_cast<const float2*>(&tp->xa[(t + e) * 8 + u]);
+        X[t + e][0] = fmaf(xa.x, X[t + e][0], bf_lo(r[2 * e]));
+        X[t + e][1] = fmaf(xa.y, X[t + e][1], bf_hi(r[2 * e]));
+        X[t + e][2] = fmaf(xa.x, X[t + e][2], bf_lo(r[2 * e + 1]));
+        X[t + e][3] = fmaf(xa.y, X[t + e][3], bf_hi(r[2 * e + 1]));
+      }
+    }
+    // ---- W^T = R^T T'^T ----
+    float W[8][4];
+    {
+      float m0, m1, up0, up1, dn0, dn1;
+      row_max(X, m0, m1);
+      row_scale(m0, up0, dn0);
+      row_scale(m1, up1, dn1);
+      uint32_t hi[8][2], lo[8][2];
+      split(X, up0, up1, hi, lo);
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) W[t][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 b[8];
+#pragma unroll
+        for (int t = 2 * k; t < 8; ++t) b[t] = tp->t[gdn_block(t, k)][lane];
+#pragma unroll
+        for (int t = 2 * k; t < 8; ++t) mma16(W[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b[t].x, b[t].y);
+#pragma unroll
+        for (int t = 2 * k; t < 8; ++t) mma16(W[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b[t].z, b[t].w);
+#pragma unroll
+        for (int t = 2 * k; t < 8; ++t) mma16(W[t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], b[t].x, b[t].y);
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float2 ts = *reinterpret_cast<const float2*>(&tp->ts[t * 8 + u]);
+        W[t][0] *= dn0 * ts.x;
+        W[t][1] *= dn0 * ts.y;
+        W[t][2] *= dn1 * ts.x;
+        W[t][3] *= dn1 * ts.y;
+      }
+    }
+    // ---- O^T = e^G S q + W^T P^T, for this warp's token tiles ----
+    {
+      float m0, m1, up0, up1, dn0, dn1;
+      row_max(W, m0, m1);
+      row_scale(m0, up0, dn0);
+      row_scale(m1, up1, dn1);
+      uint32_t hi[8][2];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        hi[t][0] = pack_h2(W[t][0] * up0, W[t][1] * up0);
+        hi[t][1] = pack_h2(W[t][2] * up1, W[t][3] * up1);
+      }
+      const int row0 = seq.row0 + c * kGdnChunk, n = min(kGdnChunk, seq.n - c * kGdnChunk);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t % NW != w) continue;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k <= t / 2; ++k) {
+          const uint2 b = tp->p[gdn_block(t, k)][lane];
+          mma16(o, hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b.x, b.y);
+        }
+        const float2 ps = *reinterpret_cast<const float2*>(&tp->ps[t * 8 + u]);
+        const float2 oa = *reinterpret_cast<const float2*>(&tp->oa[t * 8 + u]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = fmaf(e & 1 ? oa.y : oa.x, Y[t][e], o[e] * ((e < 2 ? dn0 : dn1) * (e & 1 ? ps.y : ps.x)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = t * 8 + u + (e & 1), col = vr + 8 * (e >> 1);
+          if (tok < n && col < a.dv) a.out[((size_t)(row0 + tok) * a.Hv + h) * a.dv + col] = f2bf(o[e]);
+        }
+      }
+    }
+    // ---- S' = e^{G_64} S + (e^{G_64 - G} W)^T K ----
+    {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float2 wd = *reinterpret_cast<const float2*>(&tp->wd[t * 8 + u]);
+        W[t][0] *= wd.x;
+        W[t][1] *= wd.y;
+        W[t][2] *= wd.x;
+        W[t][3] *= wd.y;
+      }
+      float m0, m1, up0, up1, dn0, dn1;
+      row_max(W, m0, m1);
+      row_scale(m0, up0, dn0);
+      row_scale(m1, up1, dn1);
+      uint32_t hi[8][2], lo[8][2];
+      split(W, up0, up1, hi, lo);
+      float D[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) D[t][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t B[4][4];
+        const int row = k * 16 + (lane & 15);
+#pragma unroll
+        for (int t2 = 0; t2 < 4; ++t2)
+          ldsm4_t(sK + row * DK * 2 + (((w * 8 + 2 * t2 + (lane >> 4)) ^ (row & 7)) << 4), B[t2]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          mma16(D[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          mma16(D[t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
+      }
+      const float keep = tp->keep[0];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        S[t][0] = fmaf(keep, S[t][0], D[t][0] * dn0);
+        S[t][1] = fmaf(keep, S[t][1], D[t][1] * dn0);
+        S[t][2] = fmaf(keep, S[t][2], D[t][2] * dn1);
+        S[t][3] = fmaf(keep, S[t][3], D[t][3] * dn1);
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok) {  // a copy never landed: no state is written, and the copies in flight are waited for
+    if (tid == 0) atomicOr(&a.ctrl->err, kErrTimeout);
+    for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait(&full[c & 1], (c >> 1) & 1);
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (vr + 8 * e < a.dv)
+        *reinterpret_cast<float2*>(So + (size_t)(vr + 8 * e) * DK + w * kGdnSlice + t * 8 + u) =
+            make_float2(S[t][2 * e], S[t][2 * e + 1]);
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_prefill(const GdnPrefillArgs& a, cudaStream_t s) {
-  k_gdn_plan<<<1, kPlanThreads, 0, s>>>(a);
-  const int blocks = a.n_seqs * a.Hv * ((a.dv + kRecurRows - 1) / kRecurRows);
-  switch (a.dk) {
-    case 64: k_gdn_recur<64><<<blocks, kRecurWarps * 32, 0, s>>>(a); break;
-    case 128: k_gdn_recur<128><<<blocks, kRecurWarps * 32, 0, s>>>(a); break;
-    default: k_gdn_recur<256><<<blocks, kRecurWarps * 32, 0, s>>>(a); break;
+// Slabs of a scan CTA: as many as shared memory holds (they share a chunk's K, Q, T' and P), but
+// no more than leave every SM a CTA.
+template <int DK>
+static int gdn_slabs(const GdnPrefillArgs& a, int n_sm) {
+  const int most = DK == 64 ? 8 : DK == 128 ? 4 : 1;
+  int slabs = 1;
+  const long long heads = (long long)a.n_seqs * a.Hv;
+  while (slabs < most && heads * ((a.dv + 2 * kGdnSlab * slabs - 1) / (2 * kGdnSlab * slabs)) * 2 > n_sm &&
+         slabs * kGdnSlab < a.dv)
+    slabs *= 2;
+  return slabs;
+}
+
+template <int DK>
+static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
+  using M = GdnScanSmem<DK>;
+  cudaError_t e = launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  const long long chunks = (long long)a.T / kGdnChunk + std::min(a.n_seqs, a.T);
+  if (chunks > 0) {
+    e = cudaFuncSetAttribute(k_gdn_chunk<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, GdnChunkSmem<DK>::kBytes);
+    if (e == cudaSuccess)
+      e = launch_pdl(k_gdn_chunk<DK>, dim3((unsigned)(chunks * a.Hk)), dim3(kChunkThreads), GdnChunkSmem<DK>::kBytes, s, a);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  a.slabs = gdn_slabs<DK>(a, n_sm);
+  const int rows = kGdnSlab * a.slabs;
+  e = cudaFuncSetAttribute(k_gdn_scan<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes(a.slabs));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_gdn_scan<DK>, dim3((unsigned)((long long)a.n_seqs * a.Hv * ((a.dv + rows - 1) / rows))),
+                    dim3(a.slabs * M::kWarps * 32), M::bytes(a.slabs), s, a);
+}
+
+cudaError_t launch_gdn_prefill(GdnPrefillArgs& a, cudaStream_t s) {
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  switch (a.dk) {
+    case 64: return launch_gdn_prefill_dk<64>(a, n_sm, s);
+    case 128: return launch_gdn_prefill_dk<128>(a, n_sm, s);
+    default: return launch_gdn_prefill_dk<256>(a, n_sm, s);
+  }
 }
 
 moe_status set_error(moe_status s, const char* fmt, ...);
@@ -142,11 +836,12 @@ static moe_status check_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs, 
   if (T < 0) return set_error(MOE_ERR_INVALID, "T must be >= 0 (got %d)", T);
   const long long blocks = (long long)n_seqs * Hv * ((dv + 15) / 16);
   if (blocks > 0x7fffffffLL) return set_error(MOE_ERR_INVALID, "n_seqs * n_v_heads * d_v too large");
+  if (((long long)T / kGdnChunk + n_seqs) * Hk > 0x7fffffffLL) return set_error(MOE_ERR_INVALID, "T * n_k_heads too large");
   return MOE_OK;
 }
 
 struct GdnPrefillLayout {
-  size_t ctrl, seqs, total;
+  size_t ctrl, hdr, seqs, order, chunks, img, tp, total;
 };
 static GdnPrefillLayout gdn_prefill_layout(const moe_gdn_shape* shape, int n_seqs, int T) {
   GdnPrefillLayout W{};
@@ -157,7 +852,14 @@ static GdnPrefillLayout gdn_prefill_layout(const moe_gdn_shape* shape, int n_seq
     return at;
   };
   W.ctrl = take(sizeof(Ctrl));
+  // the chunks of disjoint sequences of T rows: full ones, and one ragged one per sequence
+  const size_t chunks = (size_t)T / kGdnChunk + std::min(n_seqs, T);
+  W.hdr = take(sizeof(GdnHdr));
   W.seqs = take(sizeof(GdnSeq) * (size_t)n_seqs);
+  W.order = take(sizeof(int32_t) * (size_t)n_seqs);
+  W.chunks = take(sizeof(GdnChunk) * chunks);
+  W.img = take(chunks * shape->n_k_heads * 2 * kGdnChunk * shape->d_k * 2);
+  W.tp = take(chunks * shape->n_v_heads * sizeof(GdnTP));
   W.total = (size_t)round_up((int64_t)pos, kAlign);
   return W;
 }
@@ -197,8 +899,10 @@ extern "C" moe_status moe_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs
   uint8_t* w = static_cast<uint8_t*>(ws);
   GdnPrefillArgs a{n_seqs, T, shape->n_k_heads, shape->n_v_heads, shape->d_k, shape->d_v, offsets, state_in, state_out,
                    static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), g,
-                   beta, static_cast<uint16_t*>(out), reinterpret_cast<Ctrl*>(w + W.ctrl),
-                   reinterpret_cast<GdnSeq*>(w + W.seqs)};
+                   beta, static_cast<uint16_t*>(out), 1, reinterpret_cast<Ctrl*>(w + W.ctrl),
+                   reinterpret_cast<GdnHdr*>(w + W.hdr), reinterpret_cast<GdnSeq*>(w + W.seqs),
+                   reinterpret_cast<int32_t*>(w + W.order), reinterpret_cast<GdnChunk*>(w + W.chunks), w + W.img,
+                   reinterpret_cast<GdnTP*>(w + W.tp)};
   const cudaError_t e = launch_gdn_prefill(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gated delta prompt launch");
   return MOE_OK;
