@@ -16,7 +16,7 @@
 //   k_gdn_plan   one CTA: checks the row ranges, lists the chunks, orders the sequences longest
 //                first (they are the critical path)
 //   k_gdn_chunk  a CTA per chunk and key head: norms, K K^T and Q K^T on the tensor cores, the
-//                decays, T' = (I + L)^-1 diag(beta) by forward substitution and P = D o Q^ K^^T;
+//                decays, T' = (I + L)^-1 diag(beta) by block inversion and P = D o Q^ K^^T;
 //                leaves K, Q, T' and P in the operand layout of the next kernel
 //   k_gdn_scan   the sequential part, W = T' R.  A slab of 16 state rows (of one sequence and value
 //                head) belongs to d_k / 64 warps, 64 columns each, and stays in their registers as
@@ -216,7 +216,8 @@ __device__ __forceinline__ void split(const float (&v)[N][4], float up0, float u
 // ---------------------------------------------------------------------------------------
 // k_gdn_chunk
 // ---------------------------------------------------------------------------------------
-constexpr int kChunkThreads = 128;  // two warps per value head, two value heads at a time
+constexpr int kChunkThreads = 256;  // four warps per value head, two value heads at a time
+constexpr int kHeadThreads = 128;
 constexpr int kMatLd = 68;          // row stride (floats) of the 64 x 64 matrices: 16-byte rows
 
 template <int DK>
@@ -226,30 +227,84 @@ struct GdnChunkSmem {
   static constexpr int kBytes = 2 * kImg + 4 * kMat;  // K, Q; K K^T, Q K^T; L (then T') of two heads
 };
 
-// Column j of (I + L)^-1 for the rows LO .. 63 (j >= LO): t_i = [i = j] - sum_{LO <= m < i} L_im t_m.
-template <int LO>
-__device__ __forceinline__ void solve_column(const float* L, int j, float (&t)[kGdnChunk - LO]) {
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(a - b) of sums held as two floats: the difference of the heads is exact or as good as its size
+__device__ __forceinline__ float decay(float2 a, float2 b) { return ex2f((a.x - b.x) + (a.y - b.y)); }
+
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kHeadThreads) : "memory");
+}
+
+// One step of the block inversion, for a block row of B rows below a block of B columns, both with
+// their inverses in place: C <- -D (C A), A and D the inverses above and below the diagonal block
+// C.  A thread has B / 4 columns of a row.
+template <int B>
+__device__ __forceinline__ void join_blocks(float* C, const float* A, const float* D, int t, int team) {
+  constexpr int NC = B / 4;
+  const int r = t / 4, c = (t % 4) * NC;
 #pragma unroll
-  for (int i = LO; i < kGdnChunk; ++i) {
-    float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
+  for (int half = 0; half < 2; ++half) {
+    const float* x = half ? D + r * kMatLd : C + r * kMatLd;
+    const float* y = (half ? C : A) + c;
+    float s[NC] = {};
+#pragma unroll 8
+    for (int k = 0; k < B; ++k) {
+      const float f = x[k];
 #pragma unroll
-    for (int m = LO; m < i; m += 4) {
-      const float4 l = *reinterpret_cast<const float4*>(L + i * kMatLd + m);
-      s0 = fmaf(-l.x, t[m - LO], s0);
-      if (m + 1 < i) s1 = fmaf(-l.y, t[m + 1 - LO], s1);
-      if (m + 2 < i) s0 = fmaf(-l.z, t[m + 2 - LO], s0);
-      if (m + 3 < i) s1 = fmaf(-l.w, t[m + 3 - LO], s1);
+      for (int e = 0; e < NC; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(y + k * kMatLd + e);
+        s[e] = fmaf(f, v.x, s[e]);
+        s[e + 1] = fmaf(f, v.y, s[e + 1]);
+        s[e + 2] = fmaf(f, v.z, s[e + 2]);
+        s[e + 3] = fmaf(f, v.w, s[e + 3]);
+      }
     }
-    t[i - LO] = s0 + s1;
+    team_sync(team);  // every thread has read C
+#pragma unroll
+    for (int e = 0; e < NC; e += 4)
+      *reinterpret_cast<float4*>(C + r * kMatLd + c + e) =
+          half ? make_float4(-s[e], -s[e + 1], -s[e + 2], -s[e + 3]) : make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+    team_sync(team);
   }
+}
+
+// (I + L)^-1 in place of the strictly lower triangular L (zeros elsewhere), by a team of 128
+// threads: the four 16 x 16 diagonal blocks by forward substitution, a thread a column, then
+// joined to blocks of 32 and of 64.
+__device__ __forceinline__ void invert(float* L, int t, int team) {
+  if (t < kGdnChunk) {
+    const int b = t / 16, j = t % 16;
+    float* D = L + b * 16 * kMatLd + b * 16;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s[2] = {i == j ? 1.f : 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < i; ++m) s[m & 1] = fmaf(-D[i * kMatLd + m], x[m], s[m & 1]);
+      x[i] = s[0] + s[1];
+    }
+    __syncwarp();  // the block's columns are all in this warp: they have all read it
+#pragma unroll
+    for (int i = 0; i < 16; ++i) D[i * kMatLd + j] = x[i];
+  }
+  team_sync(team);
+  {
+    float* D = L + (t / 64) * 32 * (kMatLd + 1);
+    join_blocks<16>(D + 16 * kMatLd, D, D + 16 * (kMatLd + 1), t % 64, team);
+  }
+  join_blocks<32>(L + 32 * kMatLd, L, L + 32 * (kMatLd + 1), t, team);
 }
 
 template <int DK>
 __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArgs a) {
   using M = GdnChunkSmem<DK>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk], s_ts[2][kGdnChunk];
-  __shared__ double s_G[2][kGdnChunk], s_low[2][kGdnChunk];  // G_i and the least G_j up to i
+  __shared__ float s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk];
+  __shared__ float2 s_G[2][kGdnChunk], s_low[2][kGdnChunk];  // log2(e) G_i and the least of them up to i, as two floats
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
@@ -260,49 +315,87 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
   float* kk = reinterpret_cast<float*>(smem + 2 * M::kImg);
   float* qk = kk + kGdnChunk * kMatLd;
   float* Lh = qk + kGdnChunk * kMatLd;
+  const int rep = a.Hv / a.Hk, team = tid / kHeadThreads, tt = tid % kHeadThreads, tw = warp & 3;
+  float* L = Lh + team * kGdnChunk * kMatLd;
 
-  // K and Q: rows scaled to a norm in [2^10, 2^11), as fp16
-  constexpr int EPL = DK / 32;
-  for (int r = warp; r < 2 * kGdnChunk; r += kChunkThreads / 32) {
-    const int z = r >> 6, row = r & 63;
-    float x[EPL], ss = 0.f;
-    const uint16_t* src = (z ? a.q : a.k) + ((size_t)(C.row0 + row) * a.Hk + kh) * DK + lane * EPL;
-#pragma unroll
-    for (int e = 0; e < EPL; e += 2) {
-      const uint32_t w = row < C.n ? *reinterpret_cast<const uint32_t*>(src + e) : 0u;
-      x[e] = bf_lo(w);
-      x[e + 1] = bf_hi(w);
-      ss = fmaf(x[e], x[e], fmaf(x[e + 1], x[e + 1], ss));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float norm = sqrtf(ss);
-    // 2^e2 brings the norm to [2^10, 2^11).  A row of a norm below 2^-100 (it vanishes next to
-    // 1e-6), and one whose sum of squares overflows (1 / inf), is 0; infinities and NaN give NaN.
-    const int ne = (int)(__float_as_uint(norm) >> 23) - 127;
-    const bool zero = ne <= -100 || ne == 128;
-    const float up = zero ? 0.f : __uint_as_float((uint32_t)(137 - ne) << 23);
-    const float down = zero ? 0.f : __uint_as_float((uint32_t)(117 + ne) << 23);
-    if (lane == 0) {
-      const float c = zero ? 0.f : down / fmaxf(norm, 1e-6f);  // the normalised row is c times the stored one
-      if (z) s_cq[row] = c * rsqrtf((float)DK);
-      else s_ck[row] = c;
-    }
-    uint32_t h[EPL / 2];
-#pragma unroll
-    for (int e = 0; e < EPL; e += 2) h[e / 2] = pack_h2(x[e] * up, x[e + 1] * up);
-    const int col = lane * EPL;  // 16-byte piece col / 8
-    uint8_t* dst = img[z] + row * DK * 2 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
-    if constexpr (EPL == 2) *reinterpret_cast<uint32_t*>(dst) = h[0];
-    else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-  __syncthreads();
+  // K and Q: rows scaled to a norm in [2^10, 2^11), as fp16.  A row is DK / 8 pieces of 16 bytes, a
+  // lane each; all of a thread's pieces are loaded before the first is used.
+  constexpr int LPR = DK / 8, N = 2 * kGdnChunk * LPR / kChunkThreads;  // lanes per row, pieces per thread
   {
-    const uint4* src = reinterpret_cast<const uint4*>(smem);
+    uint4 piece[N];
     uint4* dst = reinterpret_cast<uint4*>(a.img + ((size_t)chunk * a.Hk + kh) * 2 * M::kImg);
-    for (int i = tid; i < 2 * M::kImg / 16; i += kChunkThreads) dst[i] = src[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = i * kChunkThreads + tid, r = x / LPR, col = x % LPR, z = r >> 6, row = r & 63;
+      piece[i] = make_uint4(0, 0, 0, 0);
+      if (row < C.n)
+        piece[i] = *reinterpret_cast<const uint4*>((z ? a.q : a.k) + ((size_t)(C.row0 + row) * a.Hk + kh) * DK + col * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = i * kChunkThreads + tid, r = x / LPR, col = x % LPR, z = r >> 6, row = r & 63;
+      float v[8], ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = word_of(piece[i], e);
+        v[2 * e] = bf_lo(w);
+        v[2 * e + 1] = bf_hi(w);
+        ss = fmaf(v[2 * e], v[2 * e], fmaf(v[2 * e + 1], v[2 * e + 1], ss));
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float norm = sqrtf(ss);
+      // 2^e2 brings the norm to [2^10, 2^11).  A row of a norm below 2^-100 (it vanishes next to
+      // 1e-6), and one whose sum of squares overflows (1 / inf), is 0; infinities and NaN give NaN.
+      const int ne = (int)(__float_as_uint(norm) >> 23) - 127;
+      const bool zero = ne <= -100 || ne == 128;
+      const float up = zero ? 0.f : __uint_as_float((uint32_t)(137 - ne) << 23);
+      const float down = zero ? 0.f : __uint_as_float((uint32_t)(117 + ne) << 23);
+      if (col == 0) {
+        const float c = zero ? 0.f : down / fmaxf(norm, 1e-6f);  // the normalised row is c times the stored one
+        if (z) s_cq[row] = c * rsqrtf((float)DK);
+        else s_ck[row] = c;
+      }
+      const uint4 h = make_uint4(pack_h2(v[0] * up, v[1] * up), pack_h2(v[2] * up, v[3] * up), pack_h2(v[4] * up, v[5] * up),
+                                 pack_h2(v[6] * up, v[7] * up));
+      const int at = r * LPR + (col ^ (row & 7));
+      reinterpret_cast<uint4*>(smem)[at] = h;
+      dst[at] = h;
+    }
   }
+  // Decays: sums in 64 bits (their differences have to be good to 24; a forgotten state's g is
+  // clamped, e^-1e4 = 0), kept as two floats, in units of log 2; one warp per head
+  auto decays = [&](int h) {
+    double x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = 2 * lane + e;
+      const float gt = t < C.n ? a.g[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+      x[e] = (gt < -1e4f ? -1e4 : (double)gt) * 1.4426950408889634;
+      s_beta[team][t] = t < C.n ? a.beta[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+    }
+    double sum = x[0] + x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    const double g1 = sum, g0 = sum - x[1];
+    double low = fmin(g0, g1);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double u = __shfl_up_sync(0xffffffffu, low, o);
+      if (lane >= o) low = fmin(low, u);
+    }
+    const double before = __shfl_up_sync(0xffffffffu, low, 1);
+    const auto two = [](double v) { return make_float2((float)v, (float)(v - (double)(float)v)); };
+    s_G[team][2 * lane] = two(g0);
+    s_G[team][2 * lane + 1] = two(g1);
+    s_low[team][2 * lane] = two(lane ? fmin(before, g0) : g0);
+    s_low[team][2 * lane + 1] = two(low);
+  };
+  if (tw == 0 && team < rep) decays(kh * rep + team);
+  __syncthreads();
   // K K^T and Q K^T, lower triangle: rows in tiles of 16 (A), columns in pairs of tiles of 8 (B)
   for (int w = warp; w < 20; w += kChunkThreads / 32) {
     const int z = w / 10, u = w % 10;  // u: (row tile i, column pair j <= i)
@@ -326,114 +419,86 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
       *reinterpret_cast<float2*>(dst + (r + 8) * kMatLd + c) = make_float2(d[t][2], d[t][3]);
     }
   }
-  const int rep = a.Hv / a.Hk, pair = warp >> 1, j = tid & 63;
-  float* L = Lh + pair * kGdnChunk * kMatLd;
+  __syncthreads();
   for (int h0 = 0; h0 < rep; h0 += 2) {
-    const bool on = h0 + pair < rep;
-    const int h = kh * rep + h0 + pair;
-    // G in 64 bits: differences of sums that may be large (a forgotten state's g is clamped: e^-1e4 = 0)
-    if (on && (warp & 1) == 0) {
-      double x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = 2 * lane + e;
-        const float gt = t < C.n ? a.g[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
-        x[e] = gt < -1e4f ? -1e4 : (double)gt;
-        s_beta[pair][t] = t < C.n ? a.beta[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
-      }
-      double sum = x[0] + x[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += u;
-      }
-      const double g1 = sum, g0 = sum - x[1];
-      double low = fmin(g0, g1);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(0xffffffffu, low, o);
-        if (lane >= o) low = fmin(low, u);
-      }
-      double before = __shfl_up_sync(0xffffffffu, low, 1);
-      s_G[pair][2 * lane] = g0;
-      s_G[pair][2 * lane + 1] = g1;
-      s_low[pair][2 * lane] = lane ? fmin(before, g0) : g0;
-      s_low[pair][2 * lane + 1] = low;
+    const bool on = h0 + team < rep;
+    const int h = kh * rep + h0 + team;
+    if (h0 > 0) {
+      if (on && tw == 0) decays(h);
+      __syncthreads();
     }
-    __syncthreads();
-    if (on) {  // thread j: column j of L
-      const double Gj = s_G[pair][j];
-      const float cj = s_ck[j];
-      for (int i = 0; i < kGdnChunk; ++i) {
-        float l = 0.f;
-        if (i > j) l = s_beta[pair][i] * expf((float)(s_G[pair][i] - Gj)) * (s_ck[i] * cj) * kk[i * kMatLd + j];
-        L[i * kMatLd + j] = l;
-      }
-    }
-    __syncthreads();
-    float t[kGdnChunk];
+    GdnTP* tp = a.tp + (size_t)chunk * a.Hv + h;
     if (on) {
-      if (j < 32) {
-        solve_column<0>(L, j, t);
-      } else {
-        float u[32];
-        solve_column<32>(L, j, u);
+      // L by rows: a warp a row, a lane the columns lane and lane + 32
+#pragma unroll 4
+      for (int i = tw; i < kGdnChunk; i += 4) {
+        const float2 Gi = s_G[team][i];
+        const float f = s_beta[team][i] * s_ck[i];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          t[i] = 0.f;
-          t[32 + i] = u[i];
+        for (int c = 0; c < 2; ++c) {
+          const int j = c * 32 + lane;
+          L[i * kMatLd + j] = j < i ? f * decay(Gi, s_G[team][j]) * s_ck[j] * kk[i * kMatLd + j] : 0.f;
         }
       }
-    }
-    __syncthreads();
-    if (on) {
-      const float bj = s_beta[pair][j];
-#pragma unroll
-      for (int i = 0; i < kGdnChunk; ++i) L[i * kMatLd + j] = t[i] * bj;
-    }
-    __syncthreads();
-    GdnTP* tp = a.tp + (size_t)chunk * a.Hv + h;
-    if (on) {  // thread j: row j's scale and factors
-      float m = 0.f;
-      for (int c = 0; c <= j; ++c) m = fmaxf(m, fabsf(L[j * kMatLd + c]));
-      float up, down;
-      row_scale(m, up, down);
-      s_ts[pair][j] = up;
-      const double G = s_G[pair][j], last = s_G[pair][kGdnChunk - 1];
-      const float eg = expf((float)G);
-      tp->ts[j] = down;
-      // P is held relative to its row's least decayed entry and times 2^10 (fp16's range)
-      tp->ps[j] = expf((float)(G - s_low[pair][j])) * 0x1p-10f;
-      tp->xa[j] = -eg * s_ck[j];
-      tp->oa[j] = eg * s_cq[j];
-      tp->wd[j] = expf((float)(last - G)) * s_ck[j];
-      if (j < 32) tp->keep[j] = expf((float)last);
-    }
-    __syncthreads();
-    if (on) {
-      for (int x = (warp & 1); x < GdnTP::kBlocks; x += 2) {
-        // block x: token tile tt, step ks
+      team_sync(team);
+      invert(L, tt, team);
+      // P: block x of 20 is (token tile, step)
+      for (int x = tw; x < GdnTP::kBlocks; x += 4) {
         const int half = x < 2 ? 0 : x < 6 ? 1 : x < 12 ? 2 : 3;
-        const int rest = x - half * (half + 1), tt = 2 * half + rest / (half + 1), ks = rest % (half + 1);
-        const int i = tt * 8 + (lane >> 2), c0 = ks * 16 + 2 * (lane & 3);
-        const float up = s_ts[pair][i];
-        const double low = s_low[pair][i];
+        const int rest = x - half * (half + 1), tile = 2 * half + rest / (half + 1), ks = rest % (half + 1);
+        const int i = tile * 8 + (lane >> 2), c0 = ks * 16 + 2 * (lane & 3);
+        const float2 low = s_low[team][i];
         const float cq = s_cq[i] * 1024.f;
-        float tv[4], pv[4];
+        float pv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c = c0 + (e & 1) + (e >> 1) * 8;
-          tv[e] = c <= i ? L[i * kMatLd + c] * up : 0.f;
-          pv[e] = c <= i ? expf((float)(low - s_G[pair][c])) * (cq * s_ck[c]) * qk[i * kMatLd + c] : 0.f;
+          pv[e] = c <= i ? decay(low, s_G[team][c]) * (cq * s_ck[c]) * qk[i * kMatLd + c] : 0.f;
         }
-        uint4 o;
-        o.x = pack_h2(tv[0], tv[1]);
-        o.y = pack_h2(tv[2], tv[3]);
-        const float2 f0 = unpack_h2(o.x), f1 = unpack_h2(o.y);
-        o.z = pack_h2(tv[0] - f0.x, tv[1] - f0.y);
-        o.w = pack_h2(tv[2] - f1.x, tv[3] - f1.y);
-        tp->t[x][lane] = o;
         tp->p[x][lane] = make_uint2(pack_h2(pv[0], pv[1]), pack_h2(pv[2], pv[3]));
+      }
+      if (tt < kGdnChunk) {  // factors of token tt
+        const float2 G = s_G[team][tt], last = s_G[team][kGdnChunk - 1], zero = make_float2(0.f, 0.f);
+        const float eg = decay(G, zero);
+        // P is held relative to its row's least decayed entry and times 2^10 (fp16's range)
+        tp->ps[tt] = decay(G, s_low[team][tt]) * 0x1p-10f;
+        tp->xa[tt] = -eg * s_ck[tt];
+        tp->oa[tt] = eg * s_cq[tt];
+        tp->wd[tt] = decay(last, G) * s_ck[tt];
+        if (tt < 32) tp->keep[tt] = decay(last, zero);
+      }
+    }
+    if (on) {
+      // T' by token tiles (a warp takes tiles tw and 7 - tw: five blocks), each row scaled to its
+      // largest element
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tile = y ? 7 - tw : tw, i = tile * 8 + (lane >> 2), c0 = 2 * (lane & 3);
+        float v[4][4], m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = k * 16 + c0 + (e & 1) + (e >> 1) * 8;
+            v[k][e] = c <= i ? L[i * kMatLd + c] * s_beta[team][c] : 0.f;
+            m = fmaxf(m, fabsf(v[k][e]));
+          }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        float up, down;
+        row_scale(m, up, down);
+        if ((lane & 3) == 0) tp->ts[i] = down;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k > tile / 2) continue;
+          uint4 o;
+          o.x = pack_h2(v[k][0] * up, v[k][1] * up);
+          o.y = pack_h2(v[k][2] * up, v[k][3] * up);
+          const float2 f0 = unpack_h2(o.x), f1 = unpack_h2(o.y);
+          o.z = pack_h2(v[k][0] * up - f0.x, v[k][1] * up - f0.y);
+          o.w = pack_h2(v[k][2] * up - f1.x, v[k][3] * up - f1.y);
+          tp->t[gdn_block(tile, k)][lane] = o;
+        }
       }
     }
     __syncthreads();
