@@ -40,6 +40,7 @@
 #include "kernels.cuh"
 #include "seqs.cuh"
 #include "sync.cuh"
+#include "tc.cuh"
 
 #include <cuda_fp16.h>
 
@@ -71,9 +72,10 @@ struct GdnTP {
   uint2 p[kBlocks][32];              // P
   float xa[kGdnChunk];               // -e^{G_i} / |k_i|: what the state recalls, in R
   float oa[kGdnChunk];               // e^{G_i} / (|q_i| sqrt(d_k))
-  float wd[kGdnChunk];               // e^{G_64 - G_i} / |k_i|
-  float ts[kGdnChunk], ps[kGdnChunk];  // scales of the rows of T' and P
-  float keep[32];                    // [0]: e^{G_64}
+  float wd[kGdnChunk];               // e^{G_64 - G_i} / |k_i|, over `wd_scale`
+  float keep;                        // e^{G_64}
+  float t_scale, p_scale, wd_scale;  // what t, p and wd are to be multiplied by (powers of two but p's)
+  float pad[28];
 };
 static_assert(sizeof(GdnTP) % 128 == 0, "bulk copies and alignment");
 // Block of token tile t (8 tokens) and step k (16 tokens), k <= t / 2
@@ -160,25 +162,47 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-// d (16 x 8, fp32) += a (16 x 16, fp16) b (16 x 8, fp16).  With g = lane / 4, u = 2 (lane % 4):
-// d0,d1 = (g, u..u+1), d2,d3 = (g + 8, u..); a0 = (g, u..), a1 = (g + 8, u..), a2 = (g, u + 8..),
-// a3 = (g + 8, u + 8..); b0 = (k u.., n g), b1 = (k u + 8.., n g).
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// d (16 x 8, fp32) += a (16 x 16, fp16) b (16 x 8, fp16); mma16z: d = a b.  With g = lane / 4,
+// u = 2 (lane % 4): d[0] = row g, columns u, u + 1, d[1] = row g + 8; a0 = (g, u..), a1 = (g + 8, u..),
+// a2 = (g, u + 8..), a3 = (g + 8, u + 8..); b0 = (k u.., n g), b1 = (k u + 8.., n g).
+__device__ __forceinline__ void mma16(float2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
+__device__ __forceinline__ void mma16z(float2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0].x), "=f"(d[0].y), "=f"(d[1].x), "=f"(d[1].y)
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t pack_h2(float2 v) {
+  const __half2 h = __float22half2_rn(v);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The power of two that brings a row whose largest element is m to [2^14, 2^15) (exact; rows of
-// zeros and of values below 2^-112 by 2^126), and its inverse.
-__device__ __forceinline__ void row_scale(float m, float& up, float& down) {
-  const int e = max((int)(__float_as_uint(m) >> 23) - 127 - 14, -126);
+// The power of two that brings a largest element m to [2^TOP, 2^{TOP + 1}) (exact; 0 and values
+// below 2^{TOP - 126} by 2^126), and its inverse.
+template <int TOP>
+__device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
+  const int e = max((int)(__float_as_uint(m) >> 23) - 127 - TOP, -126);
   up = __uint_as_float((uint32_t)(127 - e) << 23);
   down = __uint_as_float((uint32_t)(127 + e) << 23);
 }
@@ -186,31 +210,25 @@ __device__ __forceinline__ void row_scale(float m, float& up, float& down) {
 // Accumulators of N tiles of 8 columns (rows g and g + 8 of a slab) -> the largest element of
 // each of the two rows over the warp's columns.
 template <int N>
-__device__ __forceinline__ void row_max(const float (&v)[N][4], float& m0, float& m1) {
-  m0 = m1 = 0.f;
+__device__ __forceinline__ void row_max(const float2 (&v)[N][2], float (&m)[2]) {
 #pragma unroll
-  for (int t = 0; t < N; ++t) {
-    m0 = fmaxf(m0, fmaxf(fabsf(v[t][0]), fabsf(v[t][1])));
-    m1 = fmaxf(m1, fmaxf(fabsf(v[t][2]), fabsf(v[t][3])));
+  for (int e = 0; e < 2; ++e) {
+    float x[2] = {0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < N; ++t) x[t & 1] = fmaxf(x[t & 1], fmaxf(fabsf(v[t][e].x), fabsf(v[t][e].y)));
+    m[e] = fmaxf(x[0], x[1]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
   }
 }
-// hi + lo of the scaled rows, as A operands: registers (2t, 2t + 1) of the two tiles of a step of 16
-template <int N>
-__device__ __forceinline__ void split(const float (&v)[N][4], float up0, float up1, uint32_t (&hi)[N][2], uint32_t (&lo)[N][2]) {
-#pragma unroll
-  for (int t = 0; t < N; ++t) {
-    const float x0 = v[t][0] * up0, x1 = v[t][1] * up0, x2 = v[t][2] * up1, x3 = v[t][3] * up1;
-    hi[t][0] = pack_h2(x0, x1);
-    hi[t][1] = pack_h2(x2, x3);
-    const float2 h0 = unpack_h2(hi[t][0]), h1 = unpack_h2(hi[t][1]);
-    lo[t][0] = pack_h2(x0 - h0.x, x1 - h0.y);
-    lo[t][1] = pack_h2(x2 - h1.x, x3 - h1.y);
-  }
+// x = hi + lo in fp16, as A operands: a step of 16 columns takes the registers of two tiles
+__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_h2(x);
+  const float2 h = unpack_h2(hi);
+  lo = pack_h2(ffma2(h, both(-1.f), x));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -239,42 +257,61 @@ __device__ __forceinline__ void team_sync(int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kHeadThreads) : "memory");
 }
 
-// One step of the block inversion, for a block row of B rows below a block of B columns, both with
-// their inverses in place: C <- -D (C A), A and D the inverses above and below the diagonal block
-// C.  A thread has B / 4 columns of a row.
+// d (16 x 8, fp32) += a (16 x 8) b (8 x 8), both fp32 in shared memory with rows of kMatLd, as the
+// products of their tf32 heads and rests (rest times rest is below 2^-22).
+__device__ __forceinline__ void tf32_parts(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;  // 10 mantissa bits: exact in tf32
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One step of the block inversion: C <- -D (C A) for the block C of B x B below the diagonal, with
+// the inverses A above and D right of it in place.  A warp makes 16 rows and B / 2 columns (B = 16: two warps
+// a block, B = 32: four).
 template <int B>
-__device__ __forceinline__ void join_blocks(float* C, const float* A, const float* D, int t, int team) {
-  constexpr int NC = B / 4;
-  const int r = t / 4, c = (t % 4) * NC;
+__device__ __forceinline__ void join_blocks(float* C, const float* A, const float* D, int part, int lane, int team) {
+  constexpr int NT = B / 16;
+  const int g = lane >> 2, t = lane & 3, r = (part >> 1) * 16 + g, c = (part & 1) * (B / 2) + g;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const float* x = half ? D + r * kMatLd : C + r * kMatLd;
-    const float* y = (half ? C : A) + c;
-    float s[NC] = {};
-#pragma unroll 8
-    for (int k = 0; k < B; ++k) {
-      const float f = x[k];
+    const float* x = half ? D : C;
+    const float* y = half ? C : A;
+    float s[NT][4] = {};
 #pragma unroll
-      for (int e = 0; e < NC; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(y + k * kMatLd + e);
-        s[e] = fmaf(f, v.x, s[e]);
-        s[e + 1] = fmaf(f, v.y, s[e + 1]);
-        s[e + 2] = fmaf(f, v.z, s[e + 2]);
-        s[e + 3] = fmaf(f, v.w, s[e + 3]);
+    for (int k = 0; k < B; k += 8) {
+      uint32_t ah[4], al[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tf32_parts(x[(r + 8 * (e & 1)) * kMatLd + k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) tf32_parts(y[(k + t + 4 * e) * kMatLd + c + n * 8], bh[e], bl[e]);
+        mma_tf32(s[n], ah, bh[0], bh[1]);
+        mma_tf32(s[n], ah, bl[0], bl[1]);
+        mma_tf32(s[n], al, bh[0], bh[1]);
       }
     }
     team_sync(team);  // every thread has read C
 #pragma unroll
-    for (int e = 0; e < NC; e += 4)
-      *reinterpret_cast<float4*>(C + r * kMatLd + c + e) =
-          half ? make_float4(-s[e], -s[e + 1], -s[e + 2], -s[e + 3]) : make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = half ? -1.f : 1.f;
+        *reinterpret_cast<float2*>(C + (r + 8 * e) * kMatLd + (c - g) + n * 8 + 2 * t) = make_float2(f * s[n][2 * e], f * s[n][2 * e + 1]);
+      }
     team_sync(team);
   }
 }
 
 // (I + L)^-1 in place of the strictly lower triangular L (zeros elsewhere), by a team of 128
 // threads: the four 16 x 16 diagonal blocks by forward substitution, a thread a column, then
-// joined to blocks of 32 and of 64.
+// joined to blocks of 32 and of 64 on the tensor cores (on the FMA units the joins were bound by
+// shared-memory reads, 272 instead of 255 us for the 16,384 tokens and 32 heads of a batch).
 __device__ __forceinline__ void invert(float* L, int t, int team) {
   if (t < kGdnChunk) {
     const int b = t / 16, j = t % 16;
@@ -294,9 +331,9 @@ __device__ __forceinline__ void invert(float* L, int t, int team) {
   team_sync(team);
   {
     float* D = L + (t / 64) * 32 * (kMatLd + 1);
-    join_blocks<16>(D + 16 * kMatLd, D, D + 16 * (kMatLd + 1), t % 64, team);
+    join_blocks<16>(D + 16 * kMatLd, D, D + 16 * (kMatLd + 1), (t >> 5) & 1, t & 31, team);
   }
-  join_blocks<32>(L + 32 * kMatLd, L, L + 32 * (kMatLd + 1), t, team);
+  join_blocks<32>(L + 32 * kMatLd, L, L + 32 * (kMatLd + 1), t >> 5, t & 31, team);
 }
 
 template <int DK>
@@ -304,13 +341,16 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
   using M = GdnChunkSmem<DK>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk];
-  __shared__ float2 s_G[2][kGdnChunk], s_low[2][kGdnChunk];  // log2(e) G_i and the least of them up to i, as two floats
+  __shared__ float2 s_G[2][kGdnChunk];  // log2(e) G_i, as two floats
+  __shared__ float s_pm[2];             // the largest G_i - G_j, j <= i (0 where nothing grows)
+  __shared__ float s_red[2][6];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
   const int chunk = blockIdx.x / a.Hk, kh = blockIdx.x - chunk * a.Hk;
-  if (chunk >= a.hdr->n_chunks) return;
-  const GdnChunk C = a.chunks[chunk];
+  const int n_chunks = a.hdr->n_chunks;
+  const GdnChunk C = a.chunks[chunk];  // the grid is the table's size; behind n_chunks it holds anything
+  if (chunk >= n_chunks) return;
   uint8_t* img[2] = {smem, smem + M::kImg};
   float* kk = reinterpret_cast<float*>(smem + 2 * M::kImg);
   float* qk = kk + kGdnChunk * kMatLd;
@@ -356,8 +396,10 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
         if (z) s_cq[row] = c * rsqrtf((float)DK);
         else s_ck[row] = c;
       }
-      const uint4 h = make_uint4(pack_h2(v[0] * up, v[1] * up), pack_h2(v[2] * up, v[3] * up), pack_h2(v[4] * up, v[5] * up),
-                                 pack_h2(v[6] * up, v[7] * up));
+      uint32_t hv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hv[e] = pack_h2(make_float2(v[2 * e] * up, v[2 * e + 1] * up));
+      const uint4 h = make_uint4(hv[0], hv[1], hv[2], hv[3]);
       const int at = r * LPR + (col ^ (row & 7));
       reinterpret_cast<uint4*>(smem)[at] = h;
       dst[at] = h;
@@ -391,8 +433,10 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
     const auto two = [](double v) { return make_float2((float)v, (float)(v - (double)(float)v)); };
     s_G[team][2 * lane] = two(g0);
     s_G[team][2 * lane + 1] = two(g1);
-    s_low[team][2 * lane] = two(lane ? fmin(before, g0) : g0);
-    s_low[team][2 * lane + 1] = two(low);
+    float up = (float)fmax(lane ? g0 - fmin(before, g0) : 0.0, g1 - low);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+    if (lane == 0) s_pm[team] = up;
   };
   if (tw == 0 && team < rep) decays(kh * rep + team);
   __syncthreads();
@@ -402,7 +446,7 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
     const int i = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, j = u - i * (i + 1) / 2;
     const uint32_t sa = smem_u32(img[z]), sb = smem_u32(img[0]);
     const int ra = i * 16 + (lane & 15), rb = j * 16 + (lane & 7) + ((lane >> 4) << 3);
-    float d[2][4] = {};
+    float2 d[2][2] = {};
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k) {
       uint32_t A[4], B[4];
@@ -415,8 +459,8 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int r = i * 16 + (lane >> 2), c = j * 16 + t * 8 + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(dst + r * kMatLd + c) = make_float2(d[t][0], d[t][1]);
-      *reinterpret_cast<float2*>(dst + (r + 8) * kMatLd + c) = make_float2(d[t][2], d[t][3]);
+      *reinterpret_cast<float2*>(dst + r * kMatLd + c) = d[t][0];
+      *reinterpret_cast<float2*>(dst + (r + 8) * kMatLd + c) = d[t][1];
     }
   }
   __syncthreads();
@@ -430,6 +474,13 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
     GdnTP* tp = a.tp + (size_t)chunk * a.Hv + h;
     if (on) {
       // L by rows: a warp a row, a lane the columns lane and lane + 32
+      float2 Gj[2];
+      float cj[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        Gj[c] = s_G[team][c * 32 + lane];
+        cj[c] = s_ck[c * 32 + lane];
+      }
 #pragma unroll 4
       for (int i = tw; i < kGdnChunk; i += 4) {
         const float2 Gi = s_G[team][i];
@@ -437,66 +488,94 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int j = c * 32 + lane;
-          L[i * kMatLd + j] = j < i ? f * decay(Gi, s_G[team][j]) * s_ck[j] * kk[i * kMatLd + j] : 0.f;
+          float l = 0.f;
+          if (c * 32 < i) l = j < i ? f * decay(Gi, Gj[c]) * cj[c] * kk[i * kMatLd + j] : 0.f;
+          L[i * kMatLd + j] = l;
         }
       }
       team_sync(team);
       invert(L, tt, team);
-      // P: block x of 20 is (token tile, step)
+      // P: block x of 20 is (token tile, step).  Held relative to the largest decay factor (1
+      // unless a state grows) and times 2^10 (fp16's range)
+      const float pm = s_pm[team];
       for (int x = tw; x < GdnTP::kBlocks; x += 4) {
         const int half = x < 2 ? 0 : x < 6 ? 1 : x < 12 ? 2 : 3;
         const int rest = x - half * (half + 1), tile = 2 * half + rest / (half + 1), ks = rest % (half + 1);
         const int i = tile * 8 + (lane >> 2), c0 = ks * 16 + 2 * (lane & 3);
-        const float2 low = s_low[team][i];
+        float2 Gi = s_G[team][i];
+        Gi.y -= pm;
         const float cq = s_cq[i] * 1024.f;
-        float pv[4];
+        uint32_t o[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = c0 + (e & 1) + (e >> 1) * 8;
-          pv[e] = c <= i ? decay(low, s_G[team][c]) * (cq * s_ck[c]) * qk[i * kMatLd + c] : 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const int c = c0 + e * 8;
+          const float4 Gc = *reinterpret_cast<const float4*>(&s_G[team][c]);
+          const float2 ck = *reinterpret_cast<const float2*>(&s_ck[c]), x2 = *reinterpret_cast<const float2*>(qk + i * kMatLd + c);
+          const float p0 = decay(Gi, make_float2(Gc.x, Gc.y)) * (cq * ck.x) * x2.x;
+          const float p1 = decay(Gi, make_float2(Gc.z, Gc.w)) * (cq * ck.y) * x2.y;
+          o[e] = pack_h2(make_float2(c <= i ? p0 : 0.f, c + 1 <= i ? p1 : 0.f));
         }
-        tp->p[x][lane] = make_uint2(pack_h2(pv[0], pv[1]), pack_h2(pv[2], pv[3]));
+        tp->p[x][lane] = make_uint2(o[0], o[1]);
       }
-      if (tt < kGdnChunk) {  // factors of token tt
-        const float2 G = s_G[team][tt], last = s_G[team][kGdnChunk - 1], zero = make_float2(0.f, 0.f);
-        const float eg = decay(G, zero);
-        // P is held relative to its row's least decayed entry and times 2^10 (fp16's range)
-        tp->ps[tt] = decay(G, s_low[team][tt]) * 0x1p-10f;
-        tp->xa[tt] = -eg * s_ck[tt];
-        tp->oa[tt] = eg * s_cq[tt];
-        tp->wd[tt] = decay(last, G) * s_ck[tt];
-        if (tt < 32) tp->keep[tt] = decay(last, zero);
-      }
-    }
-    if (on) {
-      // T' by token tiles (a warp takes tiles tw and 7 - tw: five blocks), each row scaled to its
-      // largest element
+      // T' by token tiles (a warp takes tiles tw and 7 - tw: five blocks), scaled to its largest
+      // element, and the factors of token tt
+      float v[2][4][4], m = 0.f, wd = 0.f;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int tile = y ? 7 - tw : tw, i = tile * 8 + (lane >> 2), c0 = 2 * (lane & 3);
-        float v[4][4], m = 0.f;
+        const int tile = y ? 7 - tw : tw, i = tile * 8 + (lane >> 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = k * 16 + c0 + (e & 1) + (e >> 1) * 8;
-            v[k][e] = c <= i ? L[i * kMatLd + c] * s_beta[team][c] : 0.f;
-            m = fmaxf(m, fabsf(v[k][e]));
+          for (int e = 0; e < 4; e += 2) {
+            const int c = k * 16 + 2 * (lane & 3) + e * 4;
+            float2 x = make_float2(0.f, 0.f);
+            if (k <= tile / 2) {
+              x = *reinterpret_cast<const float2*>(L + i * kMatLd + c);
+              const float2 b = *reinterpret_cast<const float2*>(&s_beta[team][c]);
+              x = make_float2(c <= i ? x.x * b.x : 0.f, c + 1 <= i ? x.y * b.y : 0.f);
+            }
+            v[y][k][e] = x.x;
+            v[y][k][e + 1] = x.y;
+            m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
           }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        float up, down;
-        row_scale(m, up, down);
-        if ((lane & 3) == 0) tp->ts[i] = down;
+      }
+      if (tt < kGdnChunk) {
+        const float2 G = s_G[team][tt];
+        const float eg = decay(G, make_float2(0.f, 0.f));
+        wd = decay(s_G[team][kGdnChunk - 1], G) * s_ck[tt];
+        tp->xa[tt] = -eg * s_ck[tt];
+        tp->oa[tt] = eg * s_cq[tt];
+      }
+      float mw = wd;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+      }
+      if (lane == 0) {
+        s_red[team][tw] = m;
+        if (tw < 2) s_red[team][4 + tw] = mw;
+      }
+      team_sync(team);
+      float up, down, upw, downw;
+      pow2_scale<14>(fmaxf(fmaxf(s_red[team][0], s_red[team][1]), fmaxf(s_red[team][2], s_red[team][3])), up, down);
+      pow2_scale<0>(fmaxf(s_red[team][4], s_red[team][5]), upw, downw);
+      if (tt < kGdnChunk) tp->wd[tt] = wd * upw;
+      if (tt == 0) {
+        tp->keep = decay(s_G[team][kGdnChunk - 1], make_float2(0.f, 0.f));
+        tp->t_scale = down;
+        tp->p_scale = ex2f(pm) * 0x1p-10f;
+        tp->wd_scale = downw;
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tile = y ? 7 - tw : tw;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (k > tile / 2) continue;
           uint4 o;
-          o.x = pack_h2(v[k][0] * up, v[k][1] * up);
-          o.y = pack_h2(v[k][2] * up, v[k][3] * up);
-          const float2 f0 = unpack_h2(o.x), f1 = unpack_h2(o.y);
-          o.z = pack_h2(v[k][0] * up - f0.x, v[k][1] * up - f0.y);
-          o.w = pack_h2(v[k][2] * up - f1.x, v[k][3] * up - f1.y);
+          split(make_float2(v[y][k][0] * up, v[y][k][1] * up), o.x, o.z);
+          split(make_float2(v[y][k][2] * up, v[y][k][3] * up), o.y, o.w);
           tp->t[gdn_block(tile, k)][lane] = o;
         }
       }
@@ -508,9 +587,10 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
 // ---------------------------------------------------------------------------------------
 // k_gdn_scan
 // ---------------------------------------------------------------------------------------
-template <int DK>
+// NS: slices of 64 state columns of a warp
+template <int DK, int NS>
 struct GdnScanSmem {
-  static constexpr int kWarps = DK / kGdnSlice;             // warps of a slab
+  static constexpr int kWarps = DK / (kGdnSlice * NS);      // warps of a slab
   static constexpr int kImg = kGdnChunk * DK * 2;
   static constexpr int kTp = 2 * kImg;                      // stage: K, Q, T' and P, V
   static constexpr int kV = kTp + (int)sizeof(GdnTP);
@@ -524,10 +604,11 @@ struct GdnScanSmem {
 __device__ __forceinline__ void slab_sync(int slab, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(slab + 1), "r"(threads) : "memory");
 }
+__device__ __forceinline__ float4 cat(const float2 (&d)[2]) { return make_float4(d[0].x, d[0].y, d[1].x, d[1].y); }
 
-template <int DK>
+template <int DK, int NS>
 __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
-  using M = GdnScanSmem<DK>;
+  using M = GdnScanSmem<DK, NS>;
   constexpr int NW = M::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[2];
@@ -552,18 +633,15 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
   const int v0 = rb * a.slabs * kGdnSlab;       // first state row of the CTA
   const int vr = v0 + slab * kGdnSlab + g;      // this lane's rows: vr and vr + 8
   const size_t state = (size_t)s * a.Hv + h;
-  float* So = a.S_out + state * a.dv * DK;
+  const size_t s_at = (state * a.dv + vr) * DK + w * NS * kGdnSlice + u;  // this lane's first element
 
-  float S[8][4];  // tiles of 8 columns of this warp's 64
+  float2 S[NS * 8][2];  // tiles of 8 columns
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < NS * 8; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float2 x = make_float2(0.f, 0.f);
-      if (a.S_in && vr + 8 * e < a.dv)
-        x = *reinterpret_cast<const float2*>(a.S_in + (state * a.dv + vr + 8 * e) * DK + w * kGdnSlice + t * 8 + u);
-      S[t][2 * e] = x.x;
-      S[t][2 * e + 1] = x.y;
+      S[t][e] = make_float2(0.f, 0.f);
+      if (a.S_in && vr + 8 * e < a.dv) S[t][e] = *reinterpret_cast<const float2*>(a.S_in + s_at + 8 * e * DK + t * 8);
     }
 
   const bool v_wide = a.dv % 8 == 0;
@@ -596,6 +674,17 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
     cp_async_arrive(&full[c & 1]);
   };
 
+  // byte offsets of this lane's operand rows (the pieces' XOR depends on the lane alone)
+  uint32_t off_n[NS][2], off_t[NS][4];
+#pragma unroll
+  for (int sl = 0; sl < NS; ++sl) {
+    const int p0 = (w * NS + sl) * 8;  // first 16-byte piece of the slice
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2) off_n[sl][k2] = (lane & 7) * DK * 2 + (((p0 + k2 * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int t2 = 0; t2 < 4; ++t2) off_t[sl][t2] = (lane & 15) * DK * 2 + (((p0 + 2 * t2 + (lane >> 4)) ^ (lane & 7)) << 4);
+  }
+
   bool ok = true;
   int issued = 0;
   if (n_ch > 0) load(issued++);
@@ -607,62 +696,58 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
     if (c + 1 < n_ch) load(issued++);
     ok = mbar_wait(&full[c & 1], (c >> 1) & 1);
     const uint32_t st = smem_u32(smem) + (c & 1) * stage_bytes;
-    const uint32_t sK = st, sQ = st + M::kImg;
     const GdnTP* tp = reinterpret_cast<const GdnTP*>(smem + (c & 1) * stage_bytes + M::kTp);
 
     // ---- X^T = S K^T (hi, lo) and Y^T = S Q^T (hi), over this warp's columns ----
-    float X[8][4], Y[8][4];
+    float2 X[8][2], Y[8][2];
     {
-      float m0, m1, up0, up1, dn0, dn1;
-      row_max(S, m0, m1);
-      row_scale(m0, up0, dn0);
-      row_scale(m1, up1, dn1);
-      uint32_t hi[8][2], lo[8][2];
-      split(S, up0, up1, hi, lo);
+      float m[2], up[2], dn[2];
+      row_max(S, m);
+      pow2_scale<14>(m[0], up[0], dn[0]);
+      pow2_scale<14>(m[1], up[1], dn[1]);
 #pragma unroll
-      for (int tg = 0; tg < 8; tg += 4) {
-        uint32_t B[4][8];
+      for (int sl = 0; sl < NS; ++sl) {
+        uint32_t hi[8][2], lo[8][2];
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {  // K, then Q
-          float (&D)[8][4] = z ? Y : X;
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = (tg + t) * 8 + (lane & 7);
-            const uint32_t base = (z ? sQ : sK) + row * DK * 2;
+          for (int e = 0; e < 2; ++e) split(mul2(S[sl * 8 + t][e], both(up[e])), hi[t][e], lo[t][e]);
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-              uint32_t r[4];
-              ldsm4(base + (((w * 8 + k2 * 4 + (lane >> 3)) ^ (row & 7)) << 4), r);
+        for (int tg = 0; tg < 8; tg += 4) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) B[t][k2 * 4 + e] = r[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) D[tg + t][e] = 0.f;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int z = 0; z < 2; ++z) {  // K, then Q
+            uint32_t B[4][2][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-              mma16(D[tg + t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], B[t][2 * k], B[t][2 * k + 1]);
-            if (!z) {
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-                mma16(D[tg + t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], B[t][2 * k], B[t][2 * k + 1]);
+              for (int k2 = 0; k2 < 2; ++k2) ldsm4(st + z * M::kImg + (tg + t) * 8 * DK * 2 + off_n[sl][k2], B[t][k2]);
+            float2 (&D)[8][2] = z ? Y : X;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = hi[2 * k][0], a1 = hi[2 * k][1], a2 = hi[2 * k + 1][0], a3 = hi[2 * k + 1][1];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t b0 = B[t][k >> 1][2 * (k & 1)], b1 = B[t][k >> 1][2 * (k & 1) + 1];
+                if (sl == 0 && k == 0) mma16z(D[tg + t], a0, a1, a2, a3, b0, b1);
+                else mma16(D[tg + t], a0, a1, a2, a3, b0, b1);
+              }
+              if (!z) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                  mma16(D[tg + t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1],
+                        B[t][k >> 1][2 * (k & 1)], B[t][k >> 1][2 * (k & 1) + 1]);
+              }
             }
           }
         }
       }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        X[t][0] *= dn0;
-        X[t][1] *= dn0;
-        X[t][2] *= dn1;
-        X[t][3] *= dn1;
-        Y[t][0] *= dn0;
-        Y[t][1] *= dn0;
-        Y[t][2] *= dn1;
-        Y[t][3] *= dn1;
-      }
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          X[t][e] = mul2(X[t][e], both(dn[e]));
+          Y[t][e] = mul2(Y[t][e], both(dn[e]));
+        }
     }
     // ---- sums over the slab's warps (each the same, in the same order); of Y only the tiles
     // t % NW == w that this warp finishes ----
@@ -670,31 +755,28 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
       float4* xch = reinterpret_cast<float4*>(smem + 2 * stage_bytes + slab * M::kXch);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        xch[(w * 16 + t) * 32 + lane] = make_float4(X[t][0], X[t][1], X[t][2], X[t][3]);
-        if (t % NW != w) xch[(w * 16 + 8 + t) * 32 + lane] = make_float4(Y[t][0], Y[t][1], Y[t][2], Y[t][3]);
+        xch[(w * 16 + t) * 32 + lane] = cat(X[t]);
+        if (NW > 2 || t % NW != w) xch[(w * 16 + 8 + t) * 32 + lane] = cat(Y[t]);
       }
       slab_sync(slab, NW * 32);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        float4 sx = make_float4(0.f, 0.f, 0.f, 0.f), sy = sx;
 #pragma unroll
-        for (int v = 0; v < NW; ++v) {
-          const float4 x = v == w ? make_float4(X[t][0], X[t][1], X[t][2], X[t][3]) : xch[(v * 16 + t) * 32 + lane];
-          sx = make_float4(sx.x + x.x, sx.y + x.y, sx.z + x.z, sx.w + x.w);
-          if (t % NW == w) {
-            const float4 y = v == w ? make_float4(Y[t][0], Y[t][1], Y[t][2], Y[t][3]) : xch[(v * 16 + 8 + t) * 32 + lane];
-            sy = make_float4(sy.x + y.x, sy.y + y.y, sy.z + y.z, sy.w + y.w);
+        for (int z = 0; z < 2; ++z) {
+          if (z && t % NW != w) continue;
+          float2 (&D)[2] = z ? Y[t] : X[t];
+          if constexpr (NW == 2) {  // the sum of two is the same either way
+            const float4 x = xch[((1 - w) * 16 + z * 8 + t) * 32 + lane];
+            D[0] = add2(D[0], make_float2(x.x, x.y));
+            D[1] = add2(D[1], make_float2(x.z, x.w));
+          } else {
+#pragma unroll
+            for (int v = 0; v < NW; ++v) {
+              const float4 x = xch[(v * 16 + z * 8 + t) * 32 + lane];
+              D[0] = v ? add2(D[0], make_float2(x.x, x.y)) : make_float2(x.x, x.y);
+              D[1] = v ? add2(D[1], make_float2(x.z, x.w)) : make_float2(x.z, x.w);
+            }
           }
-        }
-        X[t][0] = sx.x;
-        X[t][1] = sx.y;
-        X[t][2] = sx.z;
-        X[t][3] = sx.w;
-        if (t % NW == w) {
-          Y[t][0] = sy.x;
-          Y[t][1] = sy.y;
-          Y[t][2] = sy.z;
-          Y[t][3] = sy.w;
         }
       }
     }
@@ -705,124 +787,129 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
       const int row = (t + (lane >> 4)) * 8 + (lane & 7), half = (lane >> 3) & 1;
       ldsm4_t(st + M::kV + slab * M::kVSlab + row * 32 + ((half ^ ((row >> 2) & 1)) << 4), r);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 xa = *reinterpret_cast<const float2*>(&tp->xa[(t + e) * 8 + u]);
-        X[t + e][0] = fmaf(xa.x, X[t + e][0], bf_lo(r[2 * e]));
-        X[t + e][1] = fmaf(xa.y, X[t + e][1], bf_hi(r[2 * e]));
-        X[t + e][2] = fmaf(xa.x, X[t + e][2], bf_lo(r[2 * e + 1]));
-        X[t + e][3] = fmaf(xa.y, X[t + e][3], bf_hi(r[2 * e + 1]));
+      for (int y = 0; y < 2; ++y) {
+        const float2 xa = *reinterpret_cast<const float2*>(&tp->xa[(t + y) * 8 + u]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          X[t + y][e] = ffma2(xa, X[t + y][e], make_float2(bf_lo(r[2 * y + e]), bf_hi(r[2 * y + e])));
       }
     }
-    // ---- W^T = R^T T'^T ----
-    float W[8][4];
+    // ---- W^T = R^T T'^T, left as W 2^k (W = fw * what is held) ----
+    float2 W[8][2];
+    float fw[2];
     {
-      float m0, m1, up0, up1, dn0, dn1;
-      row_max(X, m0, m1);
-      row_scale(m0, up0, dn0);
-      row_scale(m1, up1, dn1);
+      float m[2], up[2], dn[2];
+      row_max(X, m);
+      pow2_scale<14>(m[0], up[0], dn[0]);
+      pow2_scale<14>(m[1], up[1], dn[1]);
       uint32_t hi[8][2], lo[8][2];
-      split(X, up0, up1, hi, lo);
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) W[t][e] = 0.f;
+        for (int e = 0; e < 2; ++e) split(mul2(X[t][e], both(up[e])), hi[t][e], lo[t][e]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        const uint32_t h0 = hi[2 * k][0], h1 = hi[2 * k][1], h2 = hi[2 * k + 1][0], h3 = hi[2 * k + 1][1];
         uint4 b[8];
 #pragma unroll
         for (int t = 2 * k; t < 8; ++t) b[t] = tp->t[gdn_block(t, k)][lane];
 #pragma unroll
-        for (int t = 2 * k; t < 8; ++t) mma16(W[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b[t].x, b[t].y);
+        for (int t = 2 * k; t < 8; ++t) {
+          if (k == 0) mma16z(W[t], h0, h1, h2, h3, b[t].x, b[t].y);
+          else mma16(W[t], h0, h1, h2, h3, b[t].x, b[t].y);
+        }
 #pragma unroll
-        for (int t = 2 * k; t < 8; ++t) mma16(W[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b[t].z, b[t].w);
+        for (int t = 2 * k; t < 8; ++t) mma16(W[t], h0, h1, h2, h3, b[t].z, b[t].w);
 #pragma unroll
         for (int t = 2 * k; t < 8; ++t) mma16(W[t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], b[t].x, b[t].y);
       }
+      row_max(W, m);
+      const float ts = tp->t_scale;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const float2 ts = *reinterpret_cast<const float2*>(&tp->ts[t * 8 + u]);
-        W[t][0] *= dn0 * ts.x;
-        W[t][1] *= dn0 * ts.y;
-        W[t][2] *= dn1 * ts.x;
-        W[t][3] *= dn1 * ts.y;
+      for (int e = 0; e < 2; ++e) {
+        float ua, da;
+        pow2_scale<13>(m[e], ua, da);
+        fw[e] = dn[e] * (da * ts);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) W[t][e] = mul2(W[t][e], both(ua));
       }
     }
     // ---- O^T = e^G S q + W^T P^T, for this warp's token tiles ----
     {
-      float m0, m1, up0, up1, dn0, dn1;
-      row_max(W, m0, m1);
-      row_scale(m0, up0, dn0);
-      row_scale(m1, up1, dn1);
       uint32_t hi[8][2];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        hi[t][0] = pack_h2(W[t][0] * up0, W[t][1] * up0);
-        hi[t][1] = pack_h2(W[t][2] * up1, W[t][3] * up1);
+        hi[t][0] = pack_h2(W[t][0]);
+        hi[t][1] = pack_h2(W[t][1]);
       }
-      const int row0 = seq.row0 + c * kGdnChunk, n = min(kGdnChunk, seq.n - c * kGdnChunk);
+      const int n = min(kGdnChunk, seq.n - c * kGdnChunk);
+      const float ps = tp->p_scale, f0 = fw[0] * ps, f1 = fw[1] * ps;
+      uint16_t* out = a.out + ((size_t)(seq.row0 + c * kGdnChunk) * a.Hv + h) * a.dv;
+      const size_t tok_stride = (size_t)a.Hv * a.dv;
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         if (t % NW != w) continue;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 o[2];
 #pragma unroll
         for (int k = 0; k <= t / 2; ++k) {
           const uint2 b = tp->p[gdn_block(t, k)][lane];
-          mma16(o, hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b.x, b.y);
+          if (k == 0) mma16z(o, hi[0][0], hi[0][1], hi[1][0], hi[1][1], b.x, b.y);
+          else mma16(o, hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b.x, b.y);
         }
-        const float2 ps = *reinterpret_cast<const float2*>(&tp->ps[t * 8 + u]);
         const float2 oa = *reinterpret_cast<const float2*>(&tp->oa[t * 8 + u]);
+        o[0] = ffma2(oa, Y[t][0], mul2(o[0], both(f0)));
+        o[1] = ffma2(oa, Y[t][1], mul2(o[1], both(f1)));
+        if (a.dv % 2 == 0) {
+          // pairs of columns: lanes of even g take the token u of rows g, g + 1, odd ones u + 1
+          const int odd = g & 1, tok = t * 8 + u + odd, col = vr - odd;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = fmaf(e & 1 ? oa.y : oa.x, Y[t][e], o[e] * ((e < 2 ? dn0 : dn1) * (e & 1 ? ps.y : ps.x)));
+          for (int e = 0; e < 2; ++e) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[e].x : o[e].y, 4);
+            const uint32_t v = odd ? pack_bf16(got, o[e].y) : pack_bf16(o[e].x, got);
+            if (tok < n && col + 8 * e < a.dv) *reinterpret_cast<uint32_t*>(out + tok * tok_stride + col + 8 * e) = v;
+          }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = t * 8 + u + (e & 1), col = vr + 8 * (e >> 1);
-          if (tok < n && col < a.dv) a.out[((size_t)(row0 + tok) * a.Hv + h) * a.dv + col] = f2bf(o[e]);
+          for (int e = 0; e < 4; ++e) {
+            const int tok = t * 8 + u + (e & 1), col = vr + 8 * (e >> 1);
+            if (tok < n && col < a.dv) out[tok * tok_stride + col] = f2bf(e & 1 ? o[e >> 1].y : o[e >> 1].x);
+          }
         }
       }
     }
     // ---- S' = e^{G_64} S + (e^{G_64 - G} W)^T K ----
     {
+      uint32_t hi[8][2], lo[8][2];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const float2 wd = *reinterpret_cast<const float2*>(&tp->wd[t * 8 + u]);
-        W[t][0] *= wd.x;
-        W[t][1] *= wd.y;
-        W[t][2] *= wd.x;
-        W[t][3] *= wd.y;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) split(mul2(W[t][e], wd), hi[t][e], lo[t][e]);
       }
-      float m0, m1, up0, up1, dn0, dn1;
-      row_max(W, m0, m1);
-      row_scale(m0, up0, dn0);
-      row_scale(m1, up1, dn1);
-      uint32_t hi[8][2], lo[8][2];
-      split(W, up0, up1, hi, lo);
-      float D[8][4];
+      const float keep = tp->keep, ws = tp->wd_scale, f[2] = {fw[0] * ws, fw[1] * ws};
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+      for (int sl = 0; sl < NS; ++sl) {
+        float2 D[8][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) D[t][e] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          uint32_t B[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t B[4][4];
-        const int row = k * 16 + (lane & 15);
+          for (int t2 = 0; t2 < 4; ++t2) ldsm4_t(st + k * 16 * DK * 2 + off_t[sl][t2], B[t2]);
+          const uint32_t h0 = hi[2 * k][0], h1 = hi[2 * k][1], h2 = hi[2 * k + 1][0], h3 = hi[2 * k + 1][1];
 #pragma unroll
-        for (int t2 = 0; t2 < 4; ++t2)
-          ldsm4_t(sK + row * DK * 2 + (((w * 8 + 2 * t2 + (lane >> 4)) ^ (row & 7)) << 4), B[t2]);
+          for (int t = 0; t < 8; ++t) {
+            if (k == 0) mma16z(D[t], h0, h1, h2, h3, B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
+            else mma16(D[t], h0, h1, h2, h3, B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            mma16(D[t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], B[t >> 1][2 * (t & 1)],
+                  B[t >> 1][2 * (t & 1) + 1]);
+        }
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-          mma16(D[t], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          mma16(D[t], lo[2 * k][0], lo[2 * k][1], lo[2 * k + 1][0], lo[2 * k + 1][1], B[t >> 1][2 * (t & 1)], B[t >> 1][2 * (t & 1) + 1]);
-      }
-      const float keep = tp->keep[0];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        S[t][0] = fmaf(keep, S[t][0], D[t][0] * dn0);
-        S[t][1] = fmaf(keep, S[t][1], D[t][1] * dn0);
-        S[t][2] = fmaf(keep, S[t][2], D[t][2] * dn1);
-        S[t][3] = fmaf(keep, S[t][3], D[t][3] * dn1);
+          for (int e = 0; e < 2; ++e) S[sl * 8 + t][e] = ffma2(D[t][e], both(f[e]), mul2(S[sl * 8 + t][e], both(keep)));
       }
     }
   }
@@ -833,32 +920,34 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
     return;
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < NS * 8; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (vr + 8 * e < a.dv)
-        *reinterpret_cast<float2*>(So + (size_t)(vr + 8 * e) * DK + w * kGdnSlice + t * 8 + u) =
-            make_float2(S[t][2 * e], S[t][2 * e + 1]);
+      if (vr + 8 * e < a.dv) *reinterpret_cast<float2*>(a.S_out + s_at + 8 * e * DK + t * 8) = S[t][e];
 }
 
 }  // namespace
 
 // Slabs of a scan CTA: as many as shared memory holds (they share a chunk's K, Q, T' and P), but
 // no more than leave every SM a CTA.
-template <int DK>
-static int gdn_slabs(const GdnPrefillArgs& a, int n_sm) {
-  const int most = DK == 64 ? 8 : DK == 128 ? 4 : 1;
-  int slabs = 1;
+template <int DK, int NS>
+static cudaError_t launch_gdn_scan(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
+  using M = GdnScanSmem<DK, NS>;
+  const int most = DK == 256 ? NS : DK == 128 ? 4 * NS : 8;
   const long long heads = (long long)a.n_seqs * a.Hv;
-  while (slabs < most && heads * ((a.dv + 2 * kGdnSlab * slabs - 1) / (2 * kGdnSlab * slabs)) * 2 > n_sm &&
-         slabs * kGdnSlab < a.dv)
-    slabs *= 2;
-  return slabs;
+  a.slabs = 1;
+  while (a.slabs < most && heads * ((a.dv + 2 * kGdnSlab * a.slabs - 1) / (2 * kGdnSlab * a.slabs)) * 2 > n_sm &&
+         a.slabs * kGdnSlab < a.dv)
+    a.slabs *= 2;
+  const int rows = kGdnSlab * a.slabs;
+  const cudaError_t e = cudaFuncSetAttribute(k_gdn_scan<DK, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes(a.slabs));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_gdn_scan<DK, NS>, dim3((unsigned)(heads * ((a.dv + rows - 1) / rows))), dim3(a.slabs * M::kWarps * 32),
+                    M::bytes(a.slabs), s, a);
 }
 
 template <int DK>
 static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
-  using M = GdnScanSmem<DK>;
   cudaError_t e = launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   const long long chunks = (long long)a.T / kGdnChunk + std::min(a.n_seqs, a.T);
@@ -868,12 +957,11 @@ static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream
       e = launch_pdl(k_gdn_chunk<DK>, dim3((unsigned)(chunks * a.Hk)), dim3(kChunkThreads), GdnChunkSmem<DK>::kBytes, s, a);
     if (e != cudaSuccess) return e;
   }
-  a.slabs = gdn_slabs<DK>(a, n_sm);
-  const int rows = kGdnSlab * a.slabs;
-  e = cudaFuncSetAttribute(k_gdn_scan<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes(a.slabs));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_gdn_scan<DK>, dim3((unsigned)((long long)a.n_seqs * a.Hv * ((a.dv + rows - 1) / rows))),
-                    dim3(a.slabs * M::kWarps * 32), M::bytes(a.slabs), s, a);
+  if constexpr (DK > kGdnSlice) {
+    const long long slabs = (long long)a.n_seqs * a.Hv * ((a.dv + kGdnSlab - 1) / kGdnSlab);
+    if (slabs >= 4LL * n_sm) return launch_gdn_scan<DK, 2>(a, n_sm, s);
+  }
+  return launch_gdn_scan<DK, 1>(a, n_sm, s);
 }
 
 cudaError_t launch_gdn_prefill(GdnPrefillArgs& a, cudaStream_t s) {
