@@ -23,6 +23,8 @@
 //                     (P in TMEM), alternating between the tiles so that one tile's softmax
 //                     overlaps the other's products
 //     warp 9          Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
+//   k_attn_few<D>   takes the place of k_attn where a call has few rows per sequence (single
+//                   tokens): units of 16 rows on mma.sync, see there
 //   k_attn_join     joins the pieces of blocks that were cut
 //
 // What is rounded: P to bf16 (the tensor core's operand; one half step, 2^-8, of each weight),
@@ -63,12 +65,17 @@ struct AttnHdr {
 };
 
 constexpr int kAttnTile = 128;     // rows of a query tile and of a key tile
-constexpr int kAttnFill = 296;     // pieces aimed at: two per SM
+constexpr int kAttnFill = 148;     // pieces aimed at (tile kernel): one per SM
+constexpr int kAttnFillFew = 296;  // and for few rows
 constexpr int kAttnMinPiece = 4;   // key tiles of a piece at least
-constexpr int kAttnMaxSlots = 2 * kAttnFill;
+constexpr int kAttnMaxSlots = 2 * kAttnFillFew;
+constexpr int kFewRows = 16;       // rows (positions x heads of a group) of a unit of the few-rows kernel
 
 struct AttnArgs {
-  int n_seqs, T, Hq, Hkv, G, d, PT, max_kv, kv_rows, rows_slot;
+  int n_seqs, T, Hq, Hkv, G, d, max_kv, kv_rows, rows_slot;
+  int PT, BP;        // positions of a query tile and of a unit
+  int fill;          // pieces that keys are cut for; 0: nothing is cut
+  int sort;          // more units than CTAs: longest first
   float scale_log2;  // scale * log2(e)
   const int32_t *offsets, *kv_begin, *kv_len;
   uint16_t* out;
@@ -95,10 +102,11 @@ __device__ __forceinline__ int tiles_of(int seen, int np) {
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constant__ AttnArgs a) {
   __shared__ int sh[32];
   __shared__ int bins[kPlanThreads];
+  __shared__ AttnSeq s_seqs[kPlanThreads];  // calls of more sequences go through global memory
   __shared__ unsigned long long s_work;
   __shared__ int s_slots, s_recs;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int BP = 2 * a.PT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, BP = a.BP;
+  AttnSeq* seqs = a.n_seqs <= kPlanThreads ? s_seqs : a.seqs;
   pdl_launch_dependents();
   pdl_wait();
   if (tid == 0) {
@@ -111,43 +119,45 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
     const int i = base + tid;
     const bool in = i < a.n_seqs;
     const int r0 = in ? a.offsets[i] : 0, r1 = in ? a.offsets[i + 1] : 0;
+    const int kv0 = !in ? 0 : a.kv_begin ? a.kv_begin[i] : r0, len = !in ? 0 : a.kv_begin ? a.kv_len[i] : r1 - r0;
     const int before = block_excl_max(r0, seen_off, sh);
     if (!in) continue;
-    const int kv0 = a.kv_begin ? a.kv_begin[i] : r0, len = a.kv_begin ? a.kv_len[i] : r1 - r0;
     const bool ok = rows_ok(r0, r1, before, a.T) && kv0 >= 0 && len >= 0 && len <= a.max_kv && kv0 <= a.kv_rows &&
                     len <= a.kv_rows - kv0;
-    a.seqs[i] = AttnSeq{r0, ok ? r1 - r0 : -1, kv0, len};
+    seqs[i] = AttnSeq{r0, ok ? r1 - r0 : -1, kv0, len};
     if (!ok) atomicOr(&a.ctrl->err, kErrBadRange);
   }
   __syncthreads();
-  // the call's key tiles, summed over blocks and key heads
-  unsigned long long work = 0;
-  for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
-    const AttnSeq q = a.seqs[s];
-    for (int b = lane; b * BP < q.n; b += 32) work += tiles_of(q.len - q.n + b * BP + 1, min(BP, q.n - b * BP));
-  }
-  if (work) atomicAdd(&s_work, work * a.Hkv);
-  __syncthreads();
-  // Pieces of at most P tiles: with P >= work / kAttnFill the pieces of cut blocks number at
-  // most 2 work / P <= kAttnMaxSlots (a block of t > P tiles makes ceil(t / P) < 2 t / P).
-  // Little work (up to 16 tiles per SM) is cut into one piece per SM, more into two.
-  const unsigned long long fill = s_work <= 16ull * (kAttnFill / 2) ? kAttnFill / 2 : kAttnFill;
-  const int P = (int)min(max((unsigned long long)kAttnMinPiece, (s_work + fill - 1) / fill), 1ull << 24);
-  // two rounds over the blocks: count the units by size, then place them, longest first
-  for (int pass = 0; pass < 2; ++pass) {
+  // Pieces of at most P tiles: with P >= the call's key tiles (over blocks and key heads) / fill the
+  // pieces of cut blocks number at most 2 fill <= kAttnMaxSlots (a block of t > P tiles makes
+  // ceil(t / P) < 2 t / P).
+  int P = 1 << 24;
+  if (a.fill) {
+    unsigned long long work = 0;
     for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
-      const AttnSeq q = a.seqs[s];
+      const AttnSeq q = seqs[s];
+      for (int b = lane; b * BP < q.n; b += 32) work += tiles_of(q.len - q.n + b * BP + 1, min(BP, q.n - b * BP));
+    }
+    if (work) atomicAdd(&s_work, work * a.Hkv);
+    __syncthreads();
+    P = (int)min(max((unsigned long long)kAttnMinPiece, (s_work + a.fill - 1) / a.fill), 1ull << 24);
+  }
+  // Place the units; longest first (a counting sort, two rounds) where a CTA has several.
+  const float to_bin = (float)(kPlanThreads - 1) / (float)(a.fill ? P : max(1, (a.max_kv + kAttnTile - 1) / kAttnTile));
+  for (int pass = a.sort ? 0 : 1; pass < 2; ++pass) {
+    for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
+      const AttnSeq q = seqs[s];
       for (int b = lane; b * BP < q.n; b += 32) {
         const int np = min(BP, q.n - b * BP), seen = q.len - q.n + b * BP + 1, t = tiles_of(seen, np);
-        const int cut = (t + P - 1) / P;                      // pieces
-        const int len = cut > 1 ? (t + cut - 1) / cut : t;    // tiles of each but the last
-        const int pieces = cut > 1 ? (t + len - 1) / len : 1;
-        const int bin = kPlanThreads - 1 - (int)((long long)len * (kPlanThreads - 1) / P);
-        if (pass == 0) {
-          atomicAdd(&bins[bin], pieces);
-          continue;
+        int len = t, pieces = 1;
+        if (t > P) {  // equal pieces
+          pieces = (t + P - 1) / P;
+          len = (t + pieces - 1) / pieces;
+          pieces = (t + len - 1) / len;
         }
+        const int bin = a.sort ? kPlanThreads - 1 - min(kPlanThreads - 1, (int)(len * to_bin)) : 0;
         const int at = atomicAdd(&bins[bin], pieces);
+        if (pass == 0) continue;
         int slot = -1;
         if (pieces > 1) {
           slot = atomicAdd(&s_slots, pieces);
@@ -163,15 +173,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
       int total = 0;
       const int first = block_excl_sum(bins[tid], total, sh);
       bins[tid] = first;
-      if (tid == 0) a.hdr->n_units = total * a.Hkv;
       __syncthreads();
     }
   }
-  if (tid == 0) a.hdr->n_recs = s_recs;
+  // every bin ends where the next begins: the last one's end is the number of units
+  if (tid == 0) {
+    a.hdr->n_units = bins[a.sort ? kPlanThreads - 1 : 0] * a.Hkv;
+    a.hdr->n_recs = s_recs;
+  }
 }
 
 // ---------------------------------------------------------------------------------------
-// The attention kernel
+// Many rows: two query tiles of 128 rows against shared key tiles, on tcgen05
 // ---------------------------------------------------------------------------------------
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kAttnThreads = 12 * 32;  // three warpgroups (the last two warps only fill theirs)
@@ -645,84 +658,401 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   }
 }
 
-// Joins the pieces of the cut blocks: a CTA per row of a block (grid-stride), its four warps
-// share the pieces, a lane has D / 32 columns.  The pieces are added in a fixed order.
+// ---------------------------------------------------------------------------------------
+// Few rows (single tokens): 16 rows against all keys, bound by reading the keys
+// ---------------------------------------------------------------------------------------
+// A unit has at most 16 rows, the height of mma.sync's tile, so the 128-row tiles of tcgen05 would
+// be filled to an eighth at most and their chain of products, softmax and TMEM round trips (about
+// 3.3 us per 128 keys) would be longer than the keys' way from memory (1.5 us at this SM's share).
+// Here eight warps take 16 keys each of a tile of 128, on their own: scores, softmax and the sums
+// of P V stay in the warp's registers, with a running maximum of its own; the eight are joined
+// once, at the end of the unit.  A ninth warp loads the tiles by TMA.
+constexpr int kFewWarps = 8, kFewThreads = (kFewWarps + 1) * 32;
+
+template <int D>
+struct FewSmem {
+  static constexpr int kTile = kAttnTile * D * 2;        // a K or V tile
+  static constexpr int kBox = kAttnTile * 64 * 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;       // K and V tile pairs
+  static constexpr int kLd = D + 8;                      // row stride (floats) of the joined sums
+  static constexpr int kSum = kFewRows * kLd * 4;
+  static constexpr int kBytes = kStages * 2 * kTile + 2 * kSum + 1024;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d (16 x 8, fp32) += a (16 x 16, bf16) b (16 x 8, bf16); fragments as in the PTX manual
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_constant__ AttnArgs a, const uint16_t* q) {
+  using L = FewSmem<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS];
+  __shared__ float2 s_ml2[2][kFewWarps][kFewRows];  // by turns: a warp may still read one unit's while another is at the next's end
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* sums = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + NS * 2 * L::kTile);
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kFewWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  const int n_units = a.hdr->n_units;
+
+  if (warp == kFewWarps) {
+    // ------------------------------ TMA loads ------------------------------
+    if (lane == 0) {
+      int kv = 0;
+      bool ok = true;
+      for (int it = 0; ok && unit_index(it) < n_units; ++it) {
+        const int e = unit_index(it) / a.Hkv, head = unit_index(it) - e * a.Hkv;
+        const AttnUnit u = a.units[e];
+        for (int kt = u.kt0; kt < u.kt1; ++kt, ++kv) {
+          const int s = kv % NS;
+          if (!wait_or_flag(&empty[s], ((kv / NS) & 1) ^ 1, a.ctrl)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&full[s], 2 * L::kTile);
+          for (int z = 0; z < 2; ++z)
+            for (int c = 0; c < D / 64; ++c)
+              tma_3d(smem + (2 * s + z) * L::kTile + c * L::kBox, z ? &a.map_v : &a.map_k, c * 64, head, u.kv0 + kt * kAttnTile,
+                     &full[s]);
+        }
+      }
+      drain_ring(full, NS, kv, a.ctrl);
+    }
+    return;
+  }
+
+  // ------------------------------ the eight warps ------------------------------
+  const int g = lane >> 2, u2 = 2 * (lane & 3);
+  int kv = 0;
+  bool ok = true;  // after a wait that ran out the warp only keeps its place in the barriers
+  for (int it = 0; unit_index(it) < n_units; ++it) {
+    const int e = unit_index(it) / a.Hkv, head = unit_index(it) - e * a.Hkv;
+    const AttnUnit u = a.units[e];
+    const int rows = u.npos * a.G;
+    // row i of the unit is (position i / G, head i % G of the group)
+    uint32_t qa[D / 16][4];
+    int seen[2];  // keys that this lane's rows g and g + 8 see
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r, pos = row / a.G, sub = row - pos * a.G;
+      seen[r] = row < rows ? u.seen + pos : 0;
+      const uint16_t* src = q + ((size_t)(u.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + u2;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          qa[k][r + 2 * c] = row < rows ? *reinterpret_cast<const uint32_t*>(src + k * 16 + c * 8) : 0u;
+    }
+    float O[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) O[n][x] = 0.f;
+
+    for (int kt = u.kt0; kt < u.kt1; ++kt, ++kv) {
+      const int st = kv % NS;
+      if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (kv / NS) & 1) ? 1 : 0);
+        if (!ok && lane == 0) atomicOr(&a.ctrl->err, kErrTimeout);
+      }
+      if (!ok) continue;
+      const uint32_t tk = smem + 2 * st * L::kTile, tv = tk + L::kTile;
+      const int key0 = kt * kAttnTile + warp * 16;  // this warp's first key
+      float x[2][4] = {};
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = warp * 16 + n * 8 + (lane & 7);
+#pragma unroll
+        for (int k2 = 0; k2 < D / 32; ++k2) {
+          uint32_t b[4];
+          ldsm4(tk + (k2 >> 1) * L::kBox + row * 128 + ((((k2 & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4), b);
+          mma_bf16(x[n], qa[2 * k2], b[0], b[1]);
+          mma_bf16(x[n], qa[2 * k2 + 1], b[2], b[3]);
+        }
+      }
+      float mn[2] = {m[0], m[1]};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[n][i] = key0 + n * 8 + u2 + (i & 1) < seen[i >> 1] ? x[n][i] * a.scale_log2 : -INFINITY;
+          mn[i >> 1] = fmaxf(mn[i >> 1], x[n][i]);
+        }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        mn[0] = fmaxf(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], o));
+        mn[1] = fmaxf(mn[1], __shfl_xor_sync(0xffffffffu, mn[1], o));
+      }
+      // (-inf) - (-inf) is no rise
+      const bool up = mn[0] - m[0] > kRescale || mn[1] - m[1] > kRescale;
+      if (__any_sync(0xffffffffu, up)) {
+        float f[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bool mine = mn[r] - m[r] > kRescale;
+          f[r] = mine ? ex2(m[r] - mn[r]) : 1.f;
+          if (mine) m[r] = mn[r];
+          l[r] *= f[r];
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[n][i] *= f[i >> 1];
+      }
+      const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+      uint32_t p[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float p0 = ex2(x[n][0] - b0), p1 = ex2(x[n][1] - b0), p2 = ex2(x[n][2] - b1), p3 = ex2(x[n][3] - b1);
+        l[0] += p0 + p1;
+        l[1] += p2 + p3;
+        p[2 * n] = pack_bf16(p0, p1);
+        p[2 * n + 1] = pack_bf16(p2, p3);
+      }
+      // Rows behind the sequence's last key hold anything, and 0 times an infinity or NaN is NaN: this
+      // warp clears its own.
+      if (key0 + 16 > u.len) {
+        const int first = max(0, u.len - key0);
+        for (int o = first * 128 + lane * 16; o < 16 * 128; o += 512)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tv + c * L::kBox + warp * 16 * 128 + o), "r"(0) : "memory");
+        proxy_fence();  // before the next copy into the tile
+        __syncwarp();
+      }
+      const int vrow = warp * 16 + (lane & 15);
+#pragma unroll
+      for (int n2 = 0; n2 < D / 16; ++n2) {
+        uint32_t b[4];
+        ldsm4_t(tv + (n2 >> 2) * L::kBox + vrow * 128 + ((((n2 & 3) * 2 + (lane >> 4)) ^ (vrow & 7)) << 4), b);
+        mma_bf16(O[2 * n2], p, b[0], b[1]);
+        mma_bf16(O[2 * n2 + 1], p, b[2], b[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    // ---- join the eight warps ----
+    float2 (*s_ml)[kFewRows] = s_ml2[it & 1];
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+    }
+    if ((lane & 3) == 0) {
+      s_ml[warp][g] = make_float2(m[0], l[0]);
+      s_ml[warp][g + 8] = make_float2(m[1], l[1]);
+    }
+    few_sync();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w][g + 8 * r].x);
+      const float f = ex2(m[r] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        O[n][2 * r] *= f;
+        O[n][2 * r + 1] *= f;
+      }
+    }
+    float* mine = sums + (warp & 1) * (L::kSum / 4);
+#pragma unroll
+    for (int turn = 0; turn < 4; ++turn) {
+      if (warp >> 1 == turn) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float2* at = reinterpret_cast<float2*>(mine + (g + 8 * r) * L::kLd + n * 8 + u2);
+            float2 v = make_float2(O[n][2 * r], O[n][2 * r + 1]);
+            if (turn) v = fadd2p(v, *at);
+            *at = v;
+          }
+      }
+      few_sync();
+    }
+    constexpr int kPer = kFewRows * D / (kFewWarps * 32);  // columns of a thread: 4 or 8
+    const int row = tid / (D / kPer), col = (tid % (D / kPer)) * kPer;
+    if (row < rows) {
+      const int pos = row / a.G, sub = row - pos * a.G;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float2 ml = s_ml[w][row];
+        sum += ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - (top == -INFINITY ? 0.f : top));
+      }
+      float v[kPer];
+#pragma unroll
+      for (int c = 0; c < kPer; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(sums + row * L::kLd + col + c);
+        const float4 y = *reinterpret_cast<const float4*>(sums + L::kSum / 4 + row * L::kLd + col + c);
+        v[c] = x.x + y.x;
+        v[c + 1] = x.y + y.y;
+        v[c + 2] = x.z + y.z;
+        v[c + 3] = x.w + y.w;
+      }
+      if (u.slot >= 0) {
+        const size_t prow = ((size_t)u.slot * a.Hkv + head) * a.rows_slot + row;
+#pragma unroll
+        for (int c = 0; c < kPer; c += 4)
+          *reinterpret_cast<float4*>(a.part_o + prow * D + col + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        if (col == 0) a.part_ml[prow] = make_float2(top, sum);
+      } else {
+        const float inv = 1.0f / sum;
+        uint32_t o[kPer / 2];
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2) o[c / 2] = u.seen + pos > 0 ? pack_bf16(v[c] * inv, v[c + 1] * inv) : 0u;
+        uint16_t* dst = a.out + ((size_t)(u.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + col;
+        if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      }
+    }
+  }
+}
+
+// Joins the pieces of the cut blocks.  A row's pieces are added in their order; a lane has D / 32
+// columns.  Rows of many pieces (a long cache) are shared by a CTA's four warps, others take one
+// warp each.
+constexpr int kJoinShare = 16;
+
 template <int D>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a) {
   constexpr int EPL = D / 32;
-  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  __shared__ float s_o[4][D];
+  __shared__ float2 s_ml[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
   if ((int)blockIdx.x >= a.hdr->n_recs) return;
   const AttnRec rec = a.recs[blockIdx.x];
   const int rows = rec.npos * a.G;  // rows of one key head
-  for (int i = blockIdx.y; i < rows * a.Hkv; i += gridDim.y) {
+  const bool share = rec.pieces > kJoinShare;
+  const int first = share ? blockIdx.y : blockIdx.y * 4 + warp, step = share ? gridDim.y : gridDim.y * 4;
+  const int p0 = share ? warp : 0, dp = share ? 4 : 1;
+  for (int i = first; i < rows * a.Hkv; i += step) {
     const int head = i / rows, row = i - head * rows, pos = row / a.G, sub = row - pos * a.G;
-    float m = -INFINITY, l = 0.f, o[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int p = warp; p < rec.pieces; p += 4) {
-      const size_t prow = ((size_t)(rec.slot + p) * a.Hkv + head) * a.rows_slot + row;
-      const float2 ml = a.part_ml[prow];
-      float v[EPL];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) v[e] = a.part_o[prow * D + lane * EPL + e];
-      if (ml.y == 0.f) continue;  // the row sees none of this piece's keys
-      const float mn = fmaxf(m, ml.x), b = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - b), g = ex2(ml.x - b);
-      m = mn;
-      l = l * f + ml.y * g;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = o[e] * f + v[e] * g;
-    }
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
+    const size_t at0 = ((size_t)rec.slot * a.Hkv + head) * a.rows_slot + row, next = (size_t)a.Hkv * a.rows_slot;
+    // the maximum first: a lane a piece
+    float top = -INFINITY;
+    for (int p = p0 + lane * dp; p < rec.pieces; p += 32 * dp) {
+      const float2 ml = a.part_ml[at0 + p * next];
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      const float mn = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), b = mn == -INFINITY ? 0.f : mn;
-      float sum = 0.f, r = 0.f;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float b = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, o[EPL] = {};
+    for (int p = p0; p < rec.pieces; p += 8 * dp) {
+      float2 ml[8];
+      float v[8][EPL];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const size_t at = at0 + min(p + x * dp, rec.pieces - 1) * next;
+        ml[x] = a.part_ml[at];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) v[x][e] = a.part_o[at * D + lane * EPL + e];
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
+        if (p + x * dp >= rec.pieces || ml[x].y == 0.f) continue;
+        const float f = ex2(ml[x].x - b);
+        sum = fmaf(ml[x].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) o[e] = fmaf(v[x][e], f, o[e]);
+      }
+    }
+    if (share) {
+      __syncthreads();
+      if (lane == 0) s_ml[warp] = make_float2(top, sum);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
+      __syncthreads();
+      if (warp) continue;
+      top = fmaxf(fmaxf(s_ml[0].x, s_ml[1].x), fmaxf(s_ml[2].x, s_ml[3].x));
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        if (s_l[w] == 0.f) continue;
-        const float g = ex2(s_m[w] - b);
-        sum += s_l[w] * g;
-        r += s_o[w][threadIdx.x] * g;
+        if (s_ml[w].y == 0.f) continue;
+        const float f = ex2(s_ml[w].x - (top == -INFINITY ? 0.f : top));
+        sum = fmaf(s_ml[w].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) o[e] = fmaf(s_o[w][lane * EPL + e], f, o[e]);
       }
-      a.out[((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + threadIdx.x] =
-          f2bf(rec.seen + pos > 0 ? r / sum : 0.f);
     }
-    __syncthreads();
+    const float inv = 1.0f / sum;
+    uint16_t* dst = a.out + ((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + lane * EPL;
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = rec.seen + pos > 0 ? pack_bf16(o[e] * inv, o[e + 1] * inv) : 0u;
   }
 }
 
 }  // namespace
 
-// The most blocks a call can have, and the most units (see k_attn_plan).
-static long long attn_max_blocks(int n_seqs, int T, int PT) { return (long long)T / (2 * PT) + std::min(n_seqs, T); }
+// The most blocks (units before cutting) that a call can have.
+static long long attn_max_blocks(int n_seqs, int T, int BP) { return (long long)T / BP + std::min(n_seqs, T); }
 static bool attn_may_cut(int max_kv) { return max_kv > kAttnMinPiece * kAttnTile; }
+// Few rows: at most 16 per sequence on average (single tokens, or so few that 16-row units do).
+static bool attn_few(const moe_attn_shape* s, int n_seqs, int T) {
+  const int G = s->n_q_heads / s->n_kv_heads;
+  return G <= kFewRows && (long long)T * G <= (long long)kFewRows * n_seqs;
+}
 
 template <int D>
-static cudaError_t launch_attn_d(const AttnArgs& a, int n_sm, cudaStream_t s) {
-  const long long blocks = attn_max_blocks(a.n_seqs, a.T, a.PT);
-  const long long units = (blocks + (attn_may_cut(a.max_kv) ? kAttnMaxSlots : 0)) * a.Hkv;
+static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n_sm, cudaStream_t s) {
+  const long long blocks = attn_max_blocks(a.n_seqs, a.T, a.BP);
+  const bool cut = attn_may_cut(a.max_kv);
+  const long long units = (blocks + (cut ? kAttnMaxSlots : 0)) * a.Hkv;
+  a.fill = !cut ? 0 : few ? kAttnFillFew : kAttnFill;
+  a.sort = units > n_sm;
   cudaError_t e = launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(k_attn<D>, dim3((unsigned)std::min<long long>(n_sm, units)), dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
-  if (e != cudaSuccess || !attn_may_cut(a.max_kv)) return e;
+  const dim3 grid((unsigned)std::min<long long>(n_sm, units));
+  if (few) {
+    e = cudaFuncSetAttribute(k_attn_few<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
+    if (e == cudaSuccess) e = launch_pdl(k_attn_few<D>, grid, dim3(kFewThreads), FewSmem<D>::kBytes, s, a, q);
+  } else {
+    e = cudaFuncSetAttribute(k_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes);
+    if (e == cudaSuccess) e = launch_pdl(k_attn<D>, grid, dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
+  }
+  if (e != cudaSuccess || !cut) return e;
   const unsigned recs = (unsigned)std::min<long long>(blocks, kAttnMaxSlots / 2);
   return launch_pdl(k_attn_join<D>, dim3(recs, (unsigned)std::min<long long>(64, (long long)a.rows_slot * a.Hkv)), dim3(128),
                     0, s, a);
 }
 
-cudaError_t launch_attn(AttnArgs& a, const void* q, const void* k, const void* v, cudaStream_t s) {
+cudaError_t launch_attn(AttnArgs& a, bool few, const void* q, const void* k, const void* v, cudaStream_t s) {
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
@@ -734,13 +1064,14 @@ cudaError_t launch_attn(AttnArgs& a, const void* q, const void* k, const void* v
     const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if ((e = map(&a.map_q, q, a.T, a.Hq, a.G, a.PT)) != cudaSuccess) return e;
+  if (!few && (e = map(&a.map_q, q, a.T, a.Hq, a.G, a.PT)) != cudaSuccess) return e;
   // without keys no unit has a key tile and the maps are not used
   if (a.kv_rows > 0) {
     if ((e = map(&a.map_k, k, a.kv_rows, a.Hkv, 1, kAttnTile)) != cudaSuccess) return e;
     if ((e = map(&a.map_v, v, a.kv_rows, a.Hkv, 1, kAttnTile)) != cudaSuccess) return e;
   }
-  return a.d == 64 ? launch_attn_d<64>(a, n_sm, s) : launch_attn_d<128>(a, n_sm, s);
+  const uint16_t* qp = static_cast<const uint16_t*>(q);
+  return a.d == 64 ? launch_attn_d<64>(a, qp, few, n_sm, s) : launch_attn_d<128>(a, qp, few, n_sm, s);
 }
 
 moe_status set_error(moe_status s, const char* fmt, ...);
@@ -760,20 +1091,23 @@ static moe_status check_attn(const moe_attn_shape* shape, int32_t n_seqs, int32_
   if (n_seqs < 1 || n_seqs > kMaxSeqs) return set_error(MOE_ERR_INVALID, "n_seqs must be 1..%d (got %d)", kMaxSeqs, n_seqs);
   if (T < 0) return set_error(MOE_ERR_INVALID, "T must be >= 0 (got %d)", T);
   if (max_kv < 0) return set_error(MOE_ERR_INVALID, "max_kv must be >= 0 (got %d)", max_kv);
-  if (attn_max_blocks(n_seqs, T, kAttnTile / (Hq / Hkv)) * Hkv > 1LL << 30)
+  if (attn_max_blocks(n_seqs, T, 1) * Hkv > 1LL << 30)
     return set_error(MOE_ERR_INVALID, "T * n_q_heads too large");
   return MOE_OK;
 }
 
 struct AttnLayout {
   size_t ctrl, seqs, hdr, units, recs, part_o, part_ml, total;
-  int PT, rows_slot;
+  int PT, BP, rows_slot;
+  bool few;
 };
 static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, int max_kv) {
   AttnLayout W{};
   const int G = shape->n_q_heads / shape->n_kv_heads;
-  W.PT = kAttnTile / G;
-  W.rows_slot = std::min(2 * W.PT, std::max(T, 1)) * G;
+  W.few = attn_few(shape, n_seqs, T);
+  W.PT = W.few ? kFewRows / G : kAttnTile / G;
+  W.BP = W.few ? W.PT : 2 * W.PT;
+  W.rows_slot = std::min(W.BP, std::max(T, 1)) * G;
   size_t pos = 0;
   auto take = [&](size_t bytes) {
     const size_t at = (size_t)round_up((int64_t)pos, kAlign);
@@ -783,7 +1117,7 @@ static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, in
   W.ctrl = take(sizeof(Ctrl));
   W.seqs = take(sizeof(AttnSeq) * (size_t)n_seqs);
   W.hdr = take(sizeof(AttnHdr));
-  const size_t blocks = (size_t)attn_max_blocks(n_seqs, T, W.PT);
+  const size_t blocks = (size_t)attn_max_blocks(n_seqs, T, W.BP);
   // The pieces of cut blocks number at most kAttnMaxSlots over all key heads; a call whose keys
   // fit one piece cuts nothing.
   const size_t slots = attn_may_cut(max_kv) ? kAttnMaxSlots : 0;
@@ -837,6 +1171,7 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   a.G = a.Hq / a.Hkv;
   a.d = shape->d;
   a.PT = W.PT;
+  a.BP = W.BP;
   a.max_kv = max_kv;
   a.kv_rows = kv_rows;
   a.rows_slot = W.rows_slot;
@@ -854,7 +1189,7 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   a.recs = reinterpret_cast<AttnRec*>(w + W.recs);
   a.part_o = reinterpret_cast<float*>(w + W.part_o);
   a.part_ml = reinterpret_cast<float2*>(w + W.part_ml);
-  const cudaError_t e = launch_attn(a, q, k, v, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_attn(a, W.few, q, k, v, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return MOE_OK;
 }
