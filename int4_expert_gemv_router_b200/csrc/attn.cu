@@ -19,7 +19,7 @@
 //     warps 0-3, 4-7  softmax of tile A, B: a thread owns a row.  S from TMEM, running maximum and
 //                     sum, P as bf16 back into TMEM over S, O rescaled when a maximum rises by
 //                     more than 2^8, the end of the unit (O / sum, or the piece's O, m, sum)
-//     warp 8          lane 0 issues the MMAs: S = Q K^T (operands in shared memory), O += P V
+//     warp 8          issues the MMAs: S = Q K^T (operands in shared memory), O += P V
 //                     (P in TMEM), alternating between the tiles so that one tile's softmax
 //                     overlaps the other's products
 //     warp 9          Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
@@ -254,12 +254,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (TMEM) += A (TMEM, bf16 pairs: 8 columns per 16 of K) * B (shared memory)
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMAs, issued by the lane whose `lead` is set.  The whole warp runs the issuing code with the
+// same values, so that descriptors live in uniform registers: issued from a one-lane branch, each
+// MMA waits for its operands to be moved there (120 instead of 64 cycles an MMA).  A descriptor's
+// high half is a constant; a k-step moves the low one.
+// D (TMEM) += A (shared memory) * B (shared memory)
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        bool acc, bool lead) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 q, %7, 0;\n"
+      " mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((int)acc), "r"((int)lead)
+      : "memory");
+}
+// D (TMEM) += A (TMEM, bf16 pairs: 8 columns per 16 of K) * B (shared memory)
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc,
+                                        bool lead) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " mov.b64 db, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((int)acc), "r"((int)lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, bool lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"((int)lead)
       : "memory");
 }
 // V as the B operand: N (the head's columns) runs along the 128-byte rows, K along the rows.
@@ -511,76 +534,81 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
   }
   if (warp == kMmaWarp) {
-    // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
-      const uint32_t id_s = attn_idesc(kAttnTile, false), id_o = attn_idesc(D, true);
-      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};  // phases used of q_full, p_full, o_free
-      int kv = 0;                                             // tiles taken from the ring
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !wait_or_flag(bar, parity, a.ctrl)) ok = false;
-        if (s_abort) ok = false;
-        return ok;
-      };
-      auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
-        const uint64_t da = umma_desc_sw128(smem + x * L::kTile), db = umma_desc_sw128(ring + slot * L::kTile);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (uint64_t)((k / 4) * (L::kBox >> 4) + (k % 4) * 2);
-          umma_f16(tmem + x * 128, da + step, db + step, id_s, k > 0);
-        }
-        umma_commit(&s_full[x]);
-      };
-      for (int it = 0; ok && unit_index(it) < n_units && !s_abort; ++it) {
-        int head;
-        const AttnWork w = attn_work(a, unit_index(it), head);
-        if (w.n == 0) continue;
-        if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (w.nk[x] > 0) {
-            if (!wait(&q_full[x], n_q[x]++ & 1)) break;
-            tc_fence_after();
-            issue_s(x, kv % NS);
-          }
-        if (!ok) break;
-        umma_commit(&kv_empty[kv % NS]);
-        if (w.n == 1) umma_commit(&q_free);
-        for (int j = 0; j < w.n && ok; ++j) {
-          const int cv = kv + 2 * j + 1, ck = cv + 1;
-          if (!wait(&kv_full[cv % NS], (cv / NS) & 1)) break;
-          bool have_k = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j >= w.nk[x]) continue;
-            if (!wait(&p_full[x], n_p[x]++ & 1)) break;
-            if (j == 0 && !wait(&o_free[x], (n_o[x]++ & 1) ^ 1)) break;
-            tc_fence_after();
-            const uint64_t db = umma_desc_mn(ring + (cv % NS) * L::kTile, L::kBox);
-#pragma unroll
-            for (int k = 0; k < kAttnTile / 16; ++k)
-              umma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + k * 8, db + (uint64_t)(k * (2048 >> 4)), id_o,
-                          j > 0 || k > 0);
-            umma_commit(&o_done[x]);
-            if (j + 1 < w.nk[x]) {
-              // in issue order behind the product that reads P where this S goes
-              if (!have_k && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
-              have_k = true;
-              tc_fence_after();
-              issue_s(x, ck % NS);
-            }
-          }
-          if (!ok) break;
-          umma_commit(&kv_empty[cv % NS]);
-          if (j + 1 < w.n) umma_commit(&kv_empty[ck % NS]);
-          if (j + 2 == w.n) umma_commit(&q_free);
-        }
-        kv += 2 * w.n;
+    // ------------------------------ MMA issuer (the whole warp; lane 0 issues) ------------------------------
+    const bool lead = lane == 0;
+    const uint32_t id_s = attn_idesc(kAttnTile, false), id_o = attn_idesc(D, true);
+    const uint64_t dq = umma_desc_sw128(smem), dk = umma_desc_sw128(ring), dv = umma_desc_mn(ring, L::kBox);
+    const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+    constexpr uint32_t kTileStep = L::kTile >> 4;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};  // phases used of q_full, p_full, o_free
+    int kv = 0;                                             // tiles taken from the ring
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity) ? 1 : 0)) {
+        ok = false;
+        if (lead) atomicOr(&a.ctrl->err, kErrTimeout);
       }
-      if (!ok) s_abort = 1;
-      umma_commit(&drain);  // every MMA of this thread has completed once it arrives
-      if (!mbar_wait(&drain, 0)) atomicOr(&a.ctrl->err, kErrTimeout);
+      return ok;
+    };
+    auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
+      const uint32_t da = q_lo + x * kTileStep, db = __shfl_sync(0xffffffffu, k_lo + slot * kTileStep, 0);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t step = (uint32_t)((k / 4) * (L::kBox >> 4) + (k % 4) * 2);
+        umma_ss(tm + x * 128, da + step, q_hi, db + step, k_hi, id_s, k > 0, lead);
+      }
+      umma_commit_if(&s_full[x], lead);
+    };
+    for (int it = 0; ok && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
+      int head;
+      const AttnWork w = attn_work(a, unit_index(it), head);
+      if (w.n == 0) continue;
+      if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (w.nk[x] > 0) {
+          if (!wait(&q_full[x], n_q[x]++ & 1)) break;
+          tc_fence_after();
+          issue_s(x, kv % NS);
+        }
+      if (!ok) break;
+      umma_commit_if(&kv_empty[kv % NS], lead);
+      if (w.n == 1) umma_commit_if(&q_free, lead);
+      for (int j = 0; j < w.n && ok; ++j) {
+        const int cv = kv + 2 * j + 1, ck = cv + 1;
+        if (!wait(&kv_full[cv % NS], (cv / NS) & 1)) break;
+        const uint32_t db = __shfl_sync(0xffffffffu, v_lo + (cv % NS) * kTileStep, 0);
+        bool have_k = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (j >= w.nk[x]) continue;
+          if (!wait(&p_full[x], n_p[x]++ & 1)) break;
+          if (j == 0 && !wait(&o_free[x], (n_o[x]++ & 1) ^ 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kAttnTile / 16; ++k)
+            umma_ts(tm + 256 + x * 128, tm + x * 128 + k * 8, db + k * (2048 >> 4), v_hi, id_o, j > 0 || k > 0, lead);
+          umma_commit_if(&o_done[x], lead);
+          if (j + 1 < w.nk[x]) {
+            // in issue order behind the product that reads P where this S goes
+            if (!have_k && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
+            have_k = true;
+            tc_fence_after();
+            issue_s(x, ck % NS);
+          }
+        }
+        if (!ok) break;
+        umma_commit_if(&kv_empty[cv % NS], lead);
+        if (j + 1 < w.n) umma_commit_if(&kv_empty[ck % NS], lead);
+        if (j + 2 == w.n) umma_commit_if(&q_free, lead);
+      }
+      kv += 2 * w.n;
     }
+    if (!ok) s_abort = 1;
+    umma_commit_if(&drain, lead);  // every MMA of this thread has completed once it arrives
+    if (!mbar_wait(&drain, 0)) atomicOr(&a.ctrl->err, kErrTimeout);
     __syncwarp();
   } else if (warp == kLoadWarp) {
     // ------------------------------ TMA loads ------------------------------
