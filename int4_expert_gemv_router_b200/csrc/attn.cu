@@ -19,10 +19,11 @@
 //     warps 0-3, 4-7  softmax of tile A, B: a thread owns a row.  S from TMEM, running maximum and
 //                     sum, P as bf16 back into TMEM over S, O rescaled when a maximum rises by
 //                     more than 2^8, the end of the unit (O / sum, or the piece's O, m, sum)
-//     warp 8          issues the MMAs: S = Q K^T (operands in shared memory), O += P V
-//                     (P in TMEM), alternating between the tiles so that one tile's softmax
-//                     overlaps the other's products
-//     warp 9          Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
+//     warps 8, 9      issue the MMAs of tile A, B: S = Q K^T (operands in shared memory), O += P V
+//                     (P in TMEM).  One tile's softmax overlaps the other's products; a warp each,
+//                     because an issuing warp's waits and commits (about 100 cycles each) are
+//                     not hidden behind its own products
+//     warp 10         Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
 //   k_attn_few<D>   takes the place of k_attn where a call has few rows per sequence (single
 //                   tokens): units of 16 rows on mma.sync, see there
 //   k_attn_join     joins the pieces of blocks that were cut
@@ -186,8 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
 // ---------------------------------------------------------------------------------------
 // Many rows: two query tiles of 128 rows against shared key tiles, on tcgen05
 // ---------------------------------------------------------------------------------------
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kAttnThreads = 12 * 32;  // three warpgroups (the last two warps only fill theirs)
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kAttnThreads = 12 * 32;  // three warpgroups (the last warp only fills its own)
 // Registers: launched with 168 a thread (384 x 168 = 64,512), redistributed to 216 for the two
 // softmax warpgroups (a row's 128 scores stay in registers) and 72 for the third:
 // 256 x 216 + 128 x 72 = 64,512.
@@ -206,6 +207,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float2 fadd2p(float2 a, float2 b) {
   float2 d;
@@ -339,8 +345,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   using L = AttnSmem<D>;
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2], p_full[2], o_done[2], o_free[2],
-      v_fix, drain;
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2], p_half[2], p_full[2],
+      o_done[2], o_free[2], v_fix, drain[2], turn[8];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -351,18 +357,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);  // both tiles are done with it
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);  // one arrival per softmax warp
+      mbar_init(&p_half[x], 4);  // one arrival per softmax warp: the first 64 keys' P, then all
+      mbar_init(&p_full[x], 4);
+      mbar_init(&drain[x], 1);
       mbar_init(&o_done[x], 1);
       mbar_init(&o_free[x], 4);
     }
-    mbar_init(&q_free, 1);
+    for (int w = 0; w < 8; ++w) mbar_init(&turn[w], 1);
+    mbar_init(&q_free, 2);
     mbar_init(&v_fix, 1);
-    mbar_init(&drain, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -387,7 +395,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
     const bool neg = a.scale_log2 < 0.f;  // then the largest x is the smallest product: work on -S
     const float sl = fabsf(a.scale_log2);
-    int n_s = 0;  // S tiles taken so far = products with P waited for (one each)
+    int n_s = 0, n_u = 0;  // S tiles and units (with key tiles) so far
+    // Turns.  The warps w of A and B share a scheduler and its exponential unit.  Left alone the two
+    // tiles run in step (both softmaxes at once, then both waiting for products); taking the weights
+    // of tile A and tile B by turns keeps one in its products while the other is in its softmax.
+    int n_t = 0;
+    uint64_t *my_turn = &turn[warp], *next_turn = &turn[warp ^ 4];
+    if (warp >= 4 && lane == 0) mbar_arrive(next_turn);
     bool alive = true;
     for (int it = 0; alive && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
       int head;
@@ -396,6 +410,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       if (np == 0) continue;
       const int seen_r = pos < np ? w.u.seen + x * a.PT + pos : 0;  // keys this row sees (a row in use or 0)
       const int seen_0 = w.u.seen + x * a.PT;                            // the tile's first position
+      const int paired = min(w.nk[0], w.nk[1]);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nk; ++j, ++n_s) {
         if (!soft_wait(&s_full[x], n_s & 1, a.ctrl, lane)) {
@@ -426,9 +441,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
+          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-          for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][i]));
+          for (int i = 2; i < 32; i += 2) mx[c] = fmax3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
         }
         const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
         if (j == 0) {
@@ -436,12 +451,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         } else {
           const bool up = (m_new - m) * sl > kRescale;
           if (__any_sync(0xffffffffu, up)) {
-            // O holds the sums over the tiles before: wait for the last of their products
-            if (!soft_wait(&o_done[x], (n_s - 1) & 1, a.ctrl, lane)) {
-              alive = false;
-              break;
-            }
-            tc_fence_after();
+            // O holds the sums over the tiles before: the last of their products was issued before
+            // this S and is done with it
             const float f = up ? ex2((m - m_new) * sl) : 1.f;
             if (up) m = m_new;
             l *= f;
@@ -458,6 +469,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         }
         const float ms = m == -INFINITY ? 0.f : -m * sl;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (j < paired && !soft_wait(my_turn, n_t++ & 1, a.ctrl, lane)) {
+          alive = false;
+          break;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t p[32];
@@ -471,7 +486,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
             p[i] = pack_bf16(pv.x, pv.y);
           }
           tmem_st32(t_s + half * 32, p);
+          if (half == 0) {
+            tmem_st_done();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[x]);
+          }
         }
+        if (j < paired && lane == 0) mbar_arrive(next_turn);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_done();
         tc_fence_before();
@@ -481,10 +503,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       if (!alive) break;
       // the end of the unit: this row's O
       if (nk > 0) {
-        if (!soft_wait(&o_done[x], (n_s - 1) & 1, a.ctrl, lane)) {
+        if (!soft_wait(&o_done[x], n_u & 1, a.ctrl, lane)) {
           alive = false;
           break;
         }
+        ++n_u;
         tc_fence_after();
       }
       const bool mine = pos < np;
@@ -533,17 +556,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
   }
-  if (warp == kMmaWarp) {
-    // ------------------------------ MMA issuer (the whole warp; lane 0 issues) ------------------------------
+  if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ------------------------------ MMA issuer of tile x (the whole warp; lane 0 issues) ------------------------------
+    const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     const bool lead = lane == 0;
     const uint32_t id_s = attn_idesc(kAttnTile, false), id_o = attn_idesc(D, true);
-    const uint64_t dq = umma_desc_sw128(smem), dk = umma_desc_sw128(ring), dv = umma_desc_mn(ring, L::kBox);
+    const uint64_t dq = umma_desc_sw128(smem + x * L::kTile), dk = umma_desc_sw128(ring), dv = umma_desc_mn(ring, L::kBox);
     const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
-    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+    const uint32_t q_lo = __shfl_sync(0xffffffffu, (uint32_t)dq, 0), k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
     constexpr uint32_t kTileStep = L::kTile >> 4;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};  // phases used of q_full, p_full, o_free
-    int kv = 0;                                             // tiles taken from the ring
+    const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + x * 128, 0), t_o = t_s + 256;
+    int n_q = 0, n_p = 0, n_o = 0;  // phases used of q_full, p_half and p_full, o_free
+    int kv = 0;                     // tiles taken from the ring
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity) ? 1 : 0)) {
@@ -552,12 +576,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       }
       return ok;
     };
-    auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
-      const uint32_t da = q_lo + x * kTileStep, db = __shfl_sync(0xffffffffu, k_lo + slot * kTileStep, 0);
+    // Done with a tile of the ring (or with Q): once this warp's products so far are complete, or at
+    // once if it made none of it.
+    auto release = [&](uint64_t* bar, bool used) {
+      if (used) umma_commit_if(bar, lead);
+      else if (lead) mbar_arrive(bar);
+    };
+    auto issue_s = [&](int slot) {  // S = Q K^T
+      const uint32_t db = __shfl_sync(0xffffffffu, k_lo + slot * kTileStep, 0);
+      tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t step = (uint32_t)((k / 4) * (L::kBox >> 4) + (k % 4) * 2);
-        umma_ss(tm + x * 128, da + step, q_hi, db + step, k_hi, id_s, k > 0, lead);
+        umma_ss(t_s, q_lo + step, q_hi, db + step, k_hi, id_s, k > 0, lead);
       }
       umma_commit_if(&s_full[x], lead);
     };
@@ -565,50 +596,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       int head;
       const AttnWork w = attn_work(a, unit_index(it), head);
       if (w.n == 0) continue;
+      const int nk = x ? w.nk[1] : w.nk[0];
       if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (w.nk[x] > 0) {
-          if (!wait(&q_full[x], n_q[x]++ & 1)) break;
-          tc_fence_after();
-          issue_s(x, kv % NS);
-        }
-      if (!ok) break;
-      umma_commit_if(&kv_empty[kv % NS], lead);
-      if (w.n == 1) umma_commit_if(&q_free, lead);
-      for (int j = 0; j < w.n && ok; ++j) {
+      if (nk > 0) {
+        if (!wait(&q_full[x], n_q++ & 1)) break;
+        issue_s(kv % NS);
+      }
+      release(&kv_empty[kv % NS], nk > 0);
+      if (w.n == 1) release(&q_free, nk > 0);
+      for (int j = 0; j < w.n; ++j) {
         const int cv = kv + 2 * j + 1, ck = cv + 1;
         if (!wait(&kv_full[cv % NS], (cv / NS) & 1)) break;
-        const uint32_t db = __shfl_sync(0xffffffffu, v_lo + (cv % NS) * kTileStep, 0);
-        bool have_k = false;
+        if (j < nk) {
+          const uint32_t db = __shfl_sync(0xffffffffu, v_lo + (cv % NS) * kTileStep, 0);
+          if (j == 0 && !wait(&o_free[x], (n_o++ & 1) ^ 1)) break;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (j >= w.nk[x]) continue;
-          if (!wait(&p_full[x], n_p[x]++ & 1)) break;
-          if (j == 0 && !wait(&o_free[x], (n_o[x]++ & 1) ^ 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < kAttnTile / 16; ++k)
-            umma_ts(tm + 256 + x * 128, tm + x * 128 + k * 8, db + k * (2048 >> 4), v_hi, id_o, j > 0 || k > 0, lead);
-          umma_commit_if(&o_done[x], lead);
-          if (j + 1 < w.nk[x]) {
-            // in issue order behind the product that reads P where this S goes
-            if (!have_k && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
-            have_k = true;
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(half ? &p_full[x] : &p_half[x], n_p & 1)) break;
             tc_fence_after();
-            issue_s(x, ck % NS);
+#pragma unroll
+            for (int k = half * 4; k < half * 4 + 4; ++k)
+              umma_ts(t_o, t_s + k * 8, db + k * (2048 >> 4), v_hi, id_o, j > 0 || k > 0, lead);
           }
+          if (!ok) break;
+          ++n_p;
+          if (j + 1 == nk) umma_commit_if(&o_done[x], lead);
         }
-        if (!ok) break;
-        umma_commit_if(&kv_empty[cv % NS], lead);
-        if (j + 1 < w.n) umma_commit_if(&kv_empty[ck % NS], lead);
-        if (j + 2 == w.n) umma_commit_if(&q_free, lead);
+        if (j + 1 < w.n) {
+          if (!wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
+          // in issue order behind the product that reads P where this S goes
+          if (j + 1 < nk) issue_s(ck % NS);
+        }
+        release(&kv_empty[cv % NS], j < nk);
+        if (j + 1 < w.n) release(&kv_empty[ck % NS], j + 1 < nk);
+        if (j + 2 == w.n) release(&q_free, nk > 0);
       }
       kv += 2 * w.n;
     }
     if (!ok) s_abort = 1;
-    umma_commit_if(&drain, lead);  // every MMA of this thread has completed once it arrives
-    if (!mbar_wait(&drain, 0)) atomicOr(&a.ctrl->err, kErrTimeout);
+    umma_commit_if(&drain[x], lead);  // every MMA of this warp has completed once it arrives
+    if (!mbar_wait(&drain[x], 0)) atomicOr(&a.ctrl->err, kErrTimeout);
     __syncwarp();
   } else if (warp == kLoadWarp) {
     // ------------------------------ TMA loads ------------------------------
