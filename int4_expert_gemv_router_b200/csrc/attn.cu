@@ -193,6 +193,7 @@ constexpr int kAttnThreads = 12 * 32;  // three warpgroups (the last warp only f
 // softmax warpgroups (a row's 128 scores stay in registers) and 72 for the third:
 // 256 x 216 + 128 x 72 = 64,512.
 constexpr int kSoftRegs = 216, kRestRegs = 72;
+constexpr int kHalf = 64;             // keys of an S buffer: two per tile, so that one fills while the other is read
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
 
 template <int D>
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   using L = AttnSmem<D>;
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2], p_half[2], p_full[2],
-      o_done[2], o_free[2], v_fix, drain[2], turn[8];
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2][2], p_full[2][2],
+      o_prev[2], o_done[2], o_free[2], v_fix, drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -361,14 +362,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_half[x], 4);  // one arrival per softmax warp: the first 64 keys' P, then all
-      mbar_init(&p_full[x], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[x][h], 1);
+        mbar_init(&p_full[x][h], 4);  // one arrival per softmax warp
+      }
+      mbar_init(&o_prev[x], 1);
       mbar_init(&drain[x], 1);
       mbar_init(&o_done[x], 1);
       mbar_init(&o_free[x], 4);
     }
-    for (int w = 0; w < 8; ++w) mbar_init(&turn[w], 1);
     mbar_init(&q_free, 2);
     mbar_init(&v_fix, 1);
     s_abort = 0;
@@ -395,13 +397,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
     const bool neg = a.scale_log2 < 0.f;  // then the largest x is the smallest product: work on -S
     const float sl = fabsf(a.scale_log2);
-    int n_s = 0, n_u = 0;  // S tiles and units (with key tiles) so far
-    // Turns.  The warps w of A and B share a scheduler and its exponential unit.  Left alone the two
-    // tiles run in step (both softmaxes at once, then both waiting for products); taking the weights
-    // of tile A and tile B by turns keeps one in its products while the other is in its softmax.
-    int n_t = 0;
-    uint64_t *my_turn = &turn[warp], *next_turn = &turn[warp ^ 4];
-    if (warp >= 4 && lane == 0) mbar_arrive(next_turn);
+    int n_s = 0, n_u = 0;  // key tiles and units (with key tiles) so far
     bool alive = true;
     for (int it = 0; alive && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
       int head;
@@ -410,95 +406,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       if (np == 0) continue;
       const int seen_r = pos < np ? w.u.seen + x * a.PT + pos : 0;  // keys this row sees (a row in use or 0)
       const int seen_0 = w.u.seen + x * a.PT;                            // the tile's first position
-      const int paired = min(w.nk[0], w.nk[1]);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nk; ++j, ++n_s) {
-        if (!soft_wait(&s_full[x], n_s & 1, a.ctrl, lane)) {
-          alive = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t s[4][32];
+      for (int j = 0; j < nk && alive; ++j, ++n_s) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + c * 32, s[c]);
+        for (int h = 0; h < 2; ++h) {  // 64 keys each
+          if (!soft_wait(&s_full[x][h], n_s & 1, a.ctrl, lane)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t s[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_done(s[c]);
-        const int kt = w.u.kt0 + j;
-        if (neg) {
+          for (int c = 0; c < 2; ++c) tmem_ld32_async(t_s + h * kHalf + c * 32, s[c]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c) tmem_ld_done(s[c]);
+          const int key0 = (w.u.kt0 + j) * kAttnTile + h * kHalf;
+          if (neg) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[c][i] ^= 0x80000000u;
-        }
-        if ((kt + 1) * kAttnTile > seen_0) {  // a key of the tile is hidden from some row
-          const int lim = seen_r - kt * kAttnTile;
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+              for (int i = 0; i < 32; ++i) s[c][i] ^= 0x80000000u;
+          }
+          if (key0 + kHalf > seen_0) {  // a key of the half is hidden from some row
+            const int lim = seen_r - key0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i >= lim) s[c][i] = 0xff800000u;
-        }
-        float mx[4];
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= lim) s[c][i] = 0xff800000u;
+          }
+          float mx[4];
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) mx[c] = fmax3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-        }
-        const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-        if (j == 0) {
-          m = m_new;
-        } else {
-          const bool up = (m_new - m) * sl > kRescale;
-          if (__any_sync(0xffffffffu, up)) {
-            // O holds the sums over the tiles before: the last of their products was issued before
-            // this S and is done with it
-            const float f = up ? ex2((m - m_new) * sl) : 1.f;
-            if (up) m = m_new;
-            l *= f;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t* v = &s[c >> 1][(c & 1) * 16];
+            mx[c] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_async(t_o + c * 32, o);
-              tmem_ld_done(o);
+            for (int i = 2; i < 16; i += 2) mx[c] = fmax3(mx[c], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          }
+          const float m_new = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmaxf(mx[3], m));
+          if (j == 0 && h == 0) {
+            m = m_new;
+          } else {
+            const bool up = (m_new - m) * sl > kRescale;
+            if (__any_sync(0xffffffffu, up)) {
+              // O holds the sums over the keys before: wait for the last of their products.  It was
+              // issued before the next half's S, or before o_prev where there is none.
+              const bool last = h == 1 && j + 1 == nk;
+              if (!soft_wait(last ? &o_prev[x] : &s_full[x][h ^ 1], (last ? n_u : n_s + h) & 1, a.ctrl, lane)) {
+                alive = false;
+                break;
+              }
+              tc_fence_after();
+              const float f = up ? ex2((m - m_new) * sl) : 1.f;
+              if (up) m = m_new;
+              l *= f;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(t_o + c * 32, o);
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_async(t_o + c * 32, o);
+                tmem_ld_done(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(t_o + c * 32, o);
+              }
             }
           }
-        }
-        const float ms = m == -INFINITY ? 0.f : -m * sl;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        if (j < paired && !soft_wait(my_turn, n_t++ & 1, a.ctrl, lane)) {
-          alive = false;
-          break;
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+          const float ms = m == -INFINITY ? 0.f : -m * sl;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const uint32_t* sv = &s[half * 2 + (i >> 4)][(i & 15) * 2];
+            const uint32_t* sv = &s[i >> 4][(i & 15) * 2];
             const float2 e = ffma2(make_float2(__uint_as_float(sv[0]), __uint_as_float(sv[1])), make_float2(sl, sl),
                                    make_float2(ms, ms));
             const float2 pv = make_float2(ex2(e.x), ex2(e.y));
             sum[i & 1] = fadd2p(sum[i & 1], pv);
             p[i] = pack_bf16(pv.x, pv.y);
           }
-          tmem_st32(t_s + half * 32, p);
-          if (half == 0) {
-            tmem_st_done();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_half[x]);
-          }
+          tmem_st32(t_s + h * kHalf, p);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_st_done();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x][h]);
         }
-        if (j < paired && lane == 0) mbar_arrive(next_turn);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st_done();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!alive) break;
       // the end of the unit: this row's O
@@ -560,13 +551,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     // ------------------------------ MMA issuer of tile x (the whole warp; lane 0 issues) ------------------------------
     const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     const bool lead = lane == 0;
-    const uint32_t id_s = attn_idesc(kAttnTile, false), id_o = attn_idesc(D, true);
+    const uint32_t id_s = attn_idesc(kHalf, false), id_o = attn_idesc(D, true);
     const uint64_t dq = umma_desc_sw128(smem + x * L::kTile), dk = umma_desc_sw128(ring), dv = umma_desc_mn(ring, L::kBox);
     const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
     const uint32_t q_lo = __shfl_sync(0xffffffffu, (uint32_t)dq, 0), k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
-    constexpr uint32_t kTileStep = L::kTile >> 4;
+    constexpr uint32_t kTileStep = L::kTile >> 4, kHalfStep = (kHalf * 128) >> 4;  // 128-byte rows
     const uint32_t t_s = __shfl_sync(0xffffffffu, tmem + x * 128, 0), t_o = t_s + 256;
-    int n_q = 0, n_p = 0, n_o = 0;  // phases used of q_full, p_half and p_full, o_free
+    int n_q = 0, n_p = 0, n_o = 0;  // phases used of q_full, p_full, o_free
     int kv = 0;                     // tiles taken from the ring
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -582,15 +573,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       if (used) umma_commit_if(bar, lead);
       else if (lead) mbar_arrive(bar);
     };
-    auto issue_s = [&](int slot) {  // S = Q K^T
-      const uint32_t db = __shfl_sync(0xffffffffu, k_lo + slot * kTileStep, 0);
+    auto issue_s = [&](int slot, int h) {  // S = Q K^T of 64 keys
+      const uint32_t db = __shfl_sync(0xffffffffu, k_lo + slot * kTileStep, 0) + h * kHalfStep;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t step = (uint32_t)((k / 4) * (L::kBox >> 4) + (k % 4) * 2);
-        umma_ss(t_s, q_lo + step, q_hi, db + step, k_hi, id_s, k > 0, lead);
+        umma_ss(t_s + h * kHalf, q_lo + step, q_hi, db + step, k_hi, id_s, k > 0, lead);
       }
-      umma_commit_if(&s_full[x], lead);
+      umma_commit_if(&s_full[x][h], lead);
     };
     for (int it = 0; ok && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
       int head;
@@ -600,32 +591,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
       if (nk > 0) {
         if (!wait(&q_full[x], n_q++ & 1)) break;
-        issue_s(kv % NS);
+        issue_s(kv % NS, 0);
+        issue_s(kv % NS, 1);
       }
       release(&kv_empty[kv % NS], nk > 0);
       if (w.n == 1) release(&q_free, nk > 0);
       for (int j = 0; j < w.n; ++j) {
         const int cv = kv + 2 * j + 1, ck = cv + 1;
         if (!wait(&kv_full[cv % NS], (cv / NS) & 1)) break;
+        if (j + 1 < w.n && j >= nk && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
         if (j < nk) {
           const uint32_t db = __shfl_sync(0xffffffffu, v_lo + (cv % NS) * kTileStep, 0);
           if (j == 0 && !wait(&o_free[x], (n_o++ & 1) ^ 1)) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!wait(half ? &p_full[x] : &p_half[x], n_p & 1)) break;
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&p_full[x][h], n_p & 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = half * 4; k < half * 4 + 4; ++k)
-              umma_ts(t_o, t_s + k * 8, db + k * (2048 >> 4), v_hi, id_o, j > 0 || k > 0, lead);
+            for (int k = 0; k < kHalf / 16; ++k)
+              umma_ts(t_o, t_s + h * kHalf + k * 8, db + h * kHalfStep + k * (2048 >> 4), v_hi, id_o, j > 0 || h > 0 || k > 0, lead);
+            if (j + 1 == nk) umma_commit_if(h ? &o_done[x] : &o_prev[x], lead);
+            if (j + 1 < w.n) {
+              if (h == 0 && !wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
+              // in issue order behind the product that reads P where this S goes
+              if (j + 1 < nk) issue_s(ck % NS, h);
+            }
           }
           if (!ok) break;
           ++n_p;
-          if (j + 1 == nk) umma_commit_if(&o_done[x], lead);
-        }
-        if (j + 1 < w.n) {
-          if (!wait(&kv_full[ck % NS], (ck / NS) & 1)) break;
-          // in issue order behind the product that reads P where this S goes
-          if (j + 1 < nk) issue_s(ck % NS);
         }
         release(&kv_empty[cv % NS], j < nk);
         if (j + 1 < w.n) release(&kv_empty[ck % NS], j + 1 < nk);
