@@ -986,26 +986,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   }
 }
 
-// Joins the pieces of the cut blocks.  A row's pieces are added in their order; a lane has D / 32
-// columns.  Rows of many pieces (a long cache) are shared by a CTA's four warps, others take one
-// warp each.
-constexpr int kJoinShare = 16;
-
-template <int D>
+// Joins the pieces of the cut blocks; a row's pieces are added in a fixed order, a lane has D / 32
+// columns.  SHARE: a CTA's four warps share a row (few rows of many pieces), else they take one each.
+template <int D, bool SHARE>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a) {
-  constexpr int EPL = D / 32;
+  constexpr int EPL = D / 32, ROWS = SHARE ? 1 : 4;
   __shared__ float s_o[4][D];
   __shared__ float2 s_ml[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  if ((int)blockIdx.x >= a.hdr->n_recs) return;
-  const AttnRec rec = a.recs[blockIdx.x];
-  const int rows = rec.npos * a.G;  // rows of one key head
-  const bool share = rec.pieces > kJoinShare;
-  const int first = share ? blockIdx.y : blockIdx.y * 4 + warp, step = share ? gridDim.y : gridDim.y * 4;
-  const int p0 = share ? warp : 0, dp = share ? 4 : 1;
-  for (int i = first; i < rows * a.Hkv; i += step) {
+  const int n_recs = a.hdr->n_recs, groups = (a.rows_slot * a.Hkv + ROWS - 1) / ROWS;  // of a block's rows
+  const int p0 = SHARE ? warp : 0, dp = SHARE ? 4 : 1;
+  for (int item = blockIdx.x; item < n_recs * groups; item += gridDim.x) {
+    const AttnRec rec = a.recs[item / groups];
+    const int rows = rec.npos * a.G, i = item % groups * ROWS + (SHARE ? 0 : warp);
+    if (i >= rows * a.Hkv) continue;
     const int head = i / rows, row = i - head * rows, pos = row / a.G, sub = row - pos * a.G;
     const size_t at0 = ((size_t)rec.slot * a.Hkv + head) * a.rows_slot + row, next = (size_t)a.Hkv * a.rows_slot;
     // the maximum first: a lane a piece
@@ -1038,8 +1034,8 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnA
         for (int e = 0; e < EPL; ++e) o[e] = fmaf(v[x][e], f, o[e]);
       }
     }
-    if (share) {
-      __syncthreads();
+    if (SHARE) {
+      __syncthreads();  // the row before has been read
       if (lane == 0) s_ml[warp] = make_float2(top, sum);
 #pragma unroll
       for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
@@ -1095,9 +1091,9 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
     if (e == cudaSuccess) e = launch_pdl(k_attn<D>, grid, dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
   }
   if (e != cudaSuccess || !cut) return e;
-  const unsigned recs = (unsigned)std::min<long long>(blocks, kAttnMaxSlots / 2);
-  return launch_pdl(k_attn_join<D>, dim3(recs, (unsigned)std::min<long long>(64, (long long)a.rows_slot * a.Hkv)), dim3(128),
-                    0, s, a);
+  const long long rows = std::min<long long>(blocks, kAttnMaxSlots / 2) * a.rows_slot * a.Hkv;
+  return few ? launch_pdl(k_attn_join<D, true>, dim3((unsigned)std::min<long long>(rows, 8 * n_sm)), dim3(128), 0, s, a)
+             : launch_pdl(k_attn_join<D, false>, dim3((unsigned)std::min<long long>((rows + 3) / 4, 8 * n_sm)), dim3(128), 0, s, a);
 }
 
 cudaError_t launch_attn(AttnArgs& a, bool few, const void* q, const void* k, const void* v, cudaStream_t s) {
