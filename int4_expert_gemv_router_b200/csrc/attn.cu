@@ -26,7 +26,7 @@
 //     warp 10         Q, K and V tiles by TMA (128-byte swizzle), K and V through one ring
 //   k_attn_few<D>   takes the place of k_attn where a call has few rows per sequence (single
 //                   tokens): units of 16 rows on mma.sync, see there
-//   k_attn_join     joins the pieces of blocks that were cut
+//   k_attn_join     joins the pieces of blocks that k_attn had cut
 //
 // What is rounded: P to bf16 (the tensor core's operand; one half step, 2^-8, of each weight),
 // and the result.  S, O, m and the sums are fp32.  A maximum may lag the true one by up to 2^8:
@@ -57,6 +57,7 @@ struct alignas(16) AttnUnit {
   int seen;       // keys that the block's first position sees (0 or less: none); the next sees one more
   int kt0, kt1;   // key tiles
   int slot;       // -1, or the piece's place among the partial results
+  int slot0, pieces;  // the cut block's first piece and its pieces
 };
 struct alignas(16) AttnRec {  // a block cut into pieces
   int row, npos, seen, slot, pieces;
@@ -70,13 +71,15 @@ constexpr int kAttnFill = 148;     // pieces aimed at (tile kernel): one per SM
 constexpr int kAttnFillFew = 296;  // and for few rows
 constexpr int kAttnMinPiece = 4;   // key tiles of a piece at least
 constexpr int kAttnMaxSlots = 2 * kAttnFillFew;
+constexpr int kPlanSeqs = 1024;
 constexpr int kFewRows = 16;       // rows (positions x heads of a group) of a unit of the few-rows kernel
 
 struct AttnArgs {
   int n_seqs, T, Hq, Hkv, G, d, max_kv, kv_rows, rows_slot;
   int PT, BP;        // positions of a query tile and of a unit
   int fill;          // pieces that keys are cut for; 0: nothing is cut
-  int sort;          // more units than CTAs: longest first
+  int sort;          // units in order, longest first
+  int few;           // the few-rows kernel's call
   float scale_log2;  // scale * log2(e)
   const int32_t *offsets, *kv_begin, *kv_len;
   uint16_t* out;
@@ -85,6 +88,7 @@ struct AttnArgs {
   AttnHdr* hdr;
   AttnUnit* units;
   AttnRec* recs;
+  int* done;         // [2][slot * Hkv + head], few rows: pieces finished of a group, groups of a block
   float* part_o;     // [slot * Hkv + head][rows_slot][d]
   float2* part_ml;   // [slot * Hkv + head][rows_slot]: maximum (log2 units) and sum
   alignas(64) CUtensorMap map_q;
@@ -103,16 +107,16 @@ __device__ __forceinline__ int tiles_of(int seen, int np) {
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constant__ AttnArgs a) {
   __shared__ int sh[32];
   __shared__ int bins[kPlanThreads];
-  __shared__ AttnSeq s_seqs[kPlanThreads];  // calls of more sequences go through global memory
+  __shared__ AttnSeq s_seqs[kPlanSeqs];  // calls of more sequences go through global memory
   __shared__ unsigned long long s_work;
-  __shared__ int s_slots, s_recs;
+  __shared__ int s_slots, s_recs, s_blocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, BP = a.BP;
-  AttnSeq* seqs = a.n_seqs <= kPlanThreads ? s_seqs : a.seqs;
+  AttnSeq* seqs = a.n_seqs <= kPlanSeqs ? s_seqs : a.seqs;
   pdl_launch_dependents();
   pdl_wait();
   if (tid == 0) {
     s_work = 0;
-    s_slots = s_recs = 0;
+    s_slots = s_recs = s_blocks = 0;
   }
   bins[tid] = 0;
   int seen_off = 0;
@@ -135,38 +139,69 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
   int P = 1 << 24;
   if (a.fill) {
     unsigned long long work = 0;
+    int blocks = 0;
     for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
       const AttnSeq q = seqs[s];
-      for (int b = lane; b * BP < q.n; b += 32) work += tiles_of(q.len - q.n + b * BP + 1, min(BP, q.n - b * BP));
+      for (int b = lane; b * BP < q.n; b += 32) {
+        work += tiles_of(q.len - q.n + b * BP + 1, min(BP, q.n - b * BP));
+        ++blocks;
+      }
     }
-    if (work) atomicAdd(&s_work, work * a.Hkv);
+    // (per warp first: 64-bit shared atomics of 32 lanes take thousands of cycles)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      work += __shfl_xor_sync(0xffffffffu, work, o);
+      blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+    }
+    if (lane == 0 && blocks) {
+      atomicAdd(&s_work, work);
+      atomicAdd(&s_blocks, blocks);
+    }
     __syncthreads();
-    P = (int)min(max((unsigned long long)kAttnMinPiece, (s_work + a.fill - 1) / a.fill), 1ull << 24);
+    // Few blocks (U of them over the key heads): at most W / P + U <= kAttnFill pieces, one round of
+    // the SMs (one token over 60,001 keys 37 -> 29 us, against 296).
+    const float U = (float)s_blocks * (float)a.Hkv, fill = 2.f * U <= kAttnFill ? kAttnFill - U : a.fill;
+    const float per = (float)s_work * (float)a.Hkv / fill;
+    // rounded up, and never below the quotient
+    P = per < 1e7f ? max(kAttnMinPiece, (int)(per * 1.0001f + 0.9999f)) : 1 << 24;
   }
   // Place the units; longest first (a counting sort, two rounds) where a CTA has several.
   const float to_bin = (float)(kPlanThreads - 1) / (float)(a.fill ? P : max(1, (a.max_kv + kAttnTile - 1) / kAttnTile));
   for (int pass = a.sort ? 0 : 1; pass < 2; ++pass) {
     for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
       const AttnSeq q = seqs[s];
-      for (int b = lane; b * BP < q.n; b += 32) {
-        const int np = min(BP, q.n - b * BP), seen = q.len - q.n + b * BP + 1, t = tiles_of(seen, np);
-        int len = t, pieces = 1;
+      for (int b0 = 0; b0 * BP < q.n; b0 += 32) {
+        const int b = b0 + lane;
+        const bool in = b * BP < q.n;
+        const int np = min(BP, q.n - b * BP), seen = q.len - q.n + b * BP + 1, t = in ? tiles_of(seen, np) : 0;
+        int len = t, pieces = in ? 1 : 0;
         if (t > P) {  // equal pieces
           pieces = (t + P - 1) / P;
           len = (t + pieces - 1) / pieces;
           pieces = (t + len - 1) / len;
         }
         const int bin = a.sort ? kPlanThreads - 1 - min(kPlanThreads - 1, (int)(len * to_bin)) : 0;
-        const int at = atomicAdd(&bins[bin], pieces);
+        const int at = in ? atomicAdd(&bins[bin], pieces) : 0;
         if (pass == 0) continue;
-        int slot = -1;
-        if (pieces > 1) {
-          slot = atomicAdd(&s_slots, pieces);
-          a.recs[atomicAdd(&s_recs, 1)] = AttnRec{q.row0 + b * BP, np, seen, slot, pieces};
+        if (pieces == 1) a.units[at] = AttnUnit{q.row0 + b * BP, np, q.kv0, q.len, seen, 0, t, -1, 0, 1};
+        // the pieces of a cut block by the whole warp
+        for (unsigned cut = __ballot_sync(0xffffffffu, pieces > 1); cut; cut &= cut - 1) {
+          const int src = __ffs(cut) - 1;
+          int slot = 0;
+          if (lane == src) {
+            slot = atomicAdd(&s_slots, pieces);
+            if (!a.few) a.recs[atomicAdd(&s_recs, 1)] = AttnRec{q.row0 + b * BP, np, seen, slot, pieces};
+          }
+          slot = __shfl_sync(0xffffffffu, slot, src);
+          const int n = __shfl_sync(0xffffffffu, pieces, src), sz = __shfl_sync(0xffffffffu, len, src);
+          const int to = __shfl_sync(0xffffffffu, at, src), tt = __shfl_sync(0xffffffffu, t, src);
+          const int bnp = __shfl_sync(0xffffffffu, np, src), bseen = __shfl_sync(0xffffffffu, seen, src);
+          for (int i = lane; i < n; i += 32)
+            a.units[to + i] = AttnUnit{q.row0 + (b0 + src) * BP, bnp, q.kv0, q.len, bseen, i * sz, min(tt, (i + 1) * sz), slot + i, slot, n};
+          if (a.few)
+            for (int i = lane; i < n * a.Hkv; i += 32)
+              a.done[slot * a.Hkv + i] = a.done[(kAttnMaxSlots + slot) * a.Hkv + i] = 0;
         }
-        for (int i = 0; i < pieces; ++i)
-          a.units[at + i] = AttnUnit{q.row0 + b * BP, np, q.kv0, q.len, seen, i * len, min(t, (i + 1) * len),
-                                     slot < 0 ? -1 : slot + i};
       }
     }
     __syncthreads();
@@ -335,6 +370,9 @@ __device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, int idx, int& h
   return w;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 __device__ __forceinline__ bool soft_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int lane) {
   const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity) ? 1 : 0);
   if (!ok && lane == 0) atomicOr(&c->err, kErrTimeout);
@@ -376,6 +414,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kLoadWarp && lane < 3)
+    prefetch_map(lane == 0 ? &a.map_q : lane == 1 ? &a.map_k : &a.map_v);
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -753,11 +793,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[NS], empty[NS];
+  __shared__ int s_last;
   __shared__ float2 s_ml2[2][kFewWarps][kFewRows];  // by turns: a warp may still read one unit's while another is at the next's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* sums = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + NS * 2 * L::kTile);
+  if (warp == kFewWarps && lane < 2) prefetch_map(lane ? &a.map_v : &a.map_k);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -973,6 +1015,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         for (int c = 0; c < kPer; c += 4)
           *reinterpret_cast<float4*>(a.part_o + prow * D + col + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         if (col == 0) a.part_ml[prow] = make_float2(top, sum);
+        __threadfence();
       } else {
         const float inv = 1.0f / sum;
         uint32_t o[kPer / 2];
@@ -983,30 +1026,90 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
       }
     }
+    if (u.slot < 0) continue;
+    // ---- join the pieces: the CTA that finishes the last of a group joins the group in the place of
+    // its first, the one that finishes the last group joins the groups.  Up to 16 pieces are one
+    // group; more make groups of eight (one CTA alone would read a long cache's 70 pieces in 9 us,
+    // the two steps take 5) ----
+    const int size = u.pieces > 16 ? 8 : u.pieces, group = (u.slot - u.slot0) / size, groups = (u.pieces + size - 1) / size;
+    for (int level = 0; level < 2; ++level) {
+      const int count = level ? groups : min(size, u.pieces - group * size);
+      const int first = level ? u.slot0 : u.slot0 + group * size, step = level ? size : 1;
+      few_sync();  // every part of this piece (or group) is written and fenced
+      if (tid == 0) s_last = atomicAdd(&a.done[(level * kAttnMaxSlots + first) * a.Hkv + head], 1) == count - 1;
+      few_sync();
+      if (s_last == 0) break;
+      __threadfence();
+      constexpr int kLanes = D / 4;  // four columns a thread, 8 (D = 128) or 16 rows at a time
+      const bool final = level || groups == 1;
+      const size_t next = (size_t)step * a.Hkv * a.rows_slot;
+      for (int r = tid / kLanes; r < rows; r += kFewWarps * 32 / kLanes) {
+        const size_t at0 = ((size_t)first * a.Hkv + head) * a.rows_slot + r;
+        const int c4 = (tid % kLanes) * 4, pos = r / a.G, sub = r - pos * a.G;
+        float m = -INFINITY, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < count; p += 8) {
+          float2 ml[8];
+          float4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const size_t at = at0 + min(p + x, count - 1) * next;
+            ml[x] = __ldcg(&a.part_ml[at]);
+            v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + c4));
+          }
+          float mn = m;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (ml[x].y != 0.f) mn = fmaxf(mn, ml[x].x);
+          const float base = mn == -INFINITY ? 0.f : mn, back = ex2(m - base);
+          m = mn;
+          sum *= back;
+          o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
+            if (p + x >= count || ml[x].y == 0.f) continue;
+            const float f = ex2(ml[x].x - base);
+            sum = fmaf(ml[x].y, f, sum);
+            o = make_float4(fmaf(v[x].x, f, o.x), fmaf(v[x].y, f, o.y), fmaf(v[x].z, f, o.z), fmaf(v[x].w, f, o.w));
+          }
+        }
+        if (final) {
+          const float inv = 1.0f / sum;
+          uint16_t* dst = a.out + ((size_t)(u.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + c4;
+          *reinterpret_cast<uint2*>(dst) =
+              u.seen + pos > 0 ? make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+        } else {
+          // a row's lanes are in one warp: they have all read the place that is overwritten
+          __syncwarp(__activemask());
+          __stcg(reinterpret_cast<float4*>(a.part_o + at0 * D + c4), o);
+          if (c4 == 0) __stcg(&a.part_ml[at0], make_float2(m, sum));
+          __threadfence();
+        }
+      }
+      if (final) break;
+    }
   }
 }
 
-// Joins the pieces of the cut blocks; a row's pieces are added in a fixed order, a lane has D / 32
-// columns.  SHARE: a CTA's four warps share a row (few rows of many pieces), else they take one each.
-template <int D, bool SHARE>
+// Joins the pieces of the cut blocks of k_attn (k_attn_few joins its own): a warp per row, a lane has
+// D / 32 columns; a row's pieces are added in a fixed order.
+template <int D>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a) {
-  constexpr int EPL = D / 32, ROWS = SHARE ? 1 : 4;
-  __shared__ float s_o[4][D];
-  __shared__ float2 s_ml[4];
+  constexpr int EPL = D / 32, ROWS = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
   const int n_recs = a.hdr->n_recs, groups = (a.rows_slot * a.Hkv + ROWS - 1) / ROWS;  // of a block's rows
-  const int p0 = SHARE ? warp : 0, dp = SHARE ? 4 : 1;
   for (int item = blockIdx.x; item < n_recs * groups; item += gridDim.x) {
     const AttnRec rec = a.recs[item / groups];
-    const int rows = rec.npos * a.G, i = item % groups * ROWS + (SHARE ? 0 : warp);
+    const int rows = rec.npos * a.G, i = item % groups * ROWS + warp;
     if (i >= rows * a.Hkv) continue;
     const int head = i / rows, row = i - head * rows, pos = row / a.G, sub = row - pos * a.G;
     const size_t at0 = ((size_t)rec.slot * a.Hkv + head) * a.rows_slot + row, next = (size_t)a.Hkv * a.rows_slot;
     // the maximum first: a lane a piece
     float top = -INFINITY;
-    for (int p = p0 + lane * dp; p < rec.pieces; p += 32 * dp) {
+    for (int p = lane; p < rec.pieces; p += 32) {
       const float2 ml = a.part_ml[at0 + p * next];
       if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
@@ -1014,45 +1117,18 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnA
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float b = top == -INFINITY ? 0.f : top;
     float sum = 0.f, o[EPL] = {};
-    for (int p = p0; p < rec.pieces; p += 8 * dp) {
-      float2 ml[8];
-      float v[8][EPL];
+#pragma unroll 4
+    for (int p = 0; p < rec.pieces; ++p) {
+      const size_t at = at0 + p * next;
+      const float2 ml = a.part_ml[at];
+      float v[EPL];
+      if constexpr (EPL == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at * D + lane * EPL);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * EPL);
+      // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
+      const float f = ml.y == 0.f ? 0.f : ex2(ml.x - b);
+      sum = fmaf(ml.y, f, sum);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const size_t at = at0 + min(p + x * dp, rec.pieces - 1) * next;
-        ml[x] = a.part_ml[at];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) v[x][e] = a.part_o[at * D + lane * EPL + e];
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
-        if (p + x * dp >= rec.pieces || ml[x].y == 0.f) continue;
-        const float f = ex2(ml[x].x - b);
-        sum = fmaf(ml[x].y, f, sum);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = fmaf(v[x][e], f, o[e]);
-      }
-    }
-    if (SHARE) {
-      __syncthreads();  // the row before has been read
-      if (lane == 0) s_ml[warp] = make_float2(top, sum);
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
-      __syncthreads();
-      if (warp) continue;
-      top = fmaxf(fmaxf(s_ml[0].x, s_ml[1].x), fmaxf(s_ml[2].x, s_ml[3].x));
-      sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (s_ml[w].y == 0.f) continue;
-        const float f = ex2(s_ml[w].x - (top == -INFINITY ? 0.f : top));
-        sum = fmaf(s_ml[w].y, f, sum);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = fmaf(s_o[w][lane * EPL + e], f, o[e]);
-      }
+      for (int e = 0; e < EPL; ++e) o[e] = ml.y == 0.f ? o[e] : fmaf(v[e], f, o[e]);
     }
     const float inv = 1.0f / sum;
     uint16_t* dst = a.out + ((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + lane * EPL;
@@ -1079,7 +1155,11 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
   const bool cut = attn_may_cut(a.max_kv);
   const long long units = (blocks + (cut ? kAttnMaxSlots : 0)) * a.Hkv;
   a.fill = !cut ? 0 : few ? kAttnFillFew : kAttnFill;
-  a.sort = units > n_sm;
+  // longest first where a CTA has several units (100 tokens over caches of 1 to 3,000: 110 against 120
+  // us), but not where few-rows units are mostly equal pieces (32 tokens over caches of 0.2 to 8
+  // thousand: 38.5 against 36.3)
+  a.sort = units > n_sm && !(few && blocks * a.Hkv <= 2 * n_sm);
+  a.few = few;
   cudaError_t e = launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)std::min<long long>(n_sm, units));
@@ -1090,10 +1170,9 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
     e = cudaFuncSetAttribute(k_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes);
     if (e == cudaSuccess) e = launch_pdl(k_attn<D>, grid, dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
   }
-  if (e != cudaSuccess || !cut) return e;
+  if (e != cudaSuccess || few || !cut) return e;
   const long long rows = std::min<long long>(blocks, kAttnMaxSlots / 2) * a.rows_slot * a.Hkv;
-  return few ? launch_pdl(k_attn_join<D, true>, dim3((unsigned)std::min<long long>(rows, 8 * n_sm)), dim3(128), 0, s, a)
-             : launch_pdl(k_attn_join<D, false>, dim3((unsigned)std::min<long long>((rows + 3) / 4, 8 * n_sm)), dim3(128), 0, s, a);
+  return launch_pdl(k_attn_join<D>, dim3((unsigned)std::min<long long>((rows + 3) / 4, 8 * n_sm)), dim3(128), 0, s, a);
 }
 
 cudaError_t launch_attn(AttnArgs& a, bool few, const void* q, const void* k, const void* v, cudaStream_t s) {
@@ -1141,7 +1220,7 @@ static moe_status check_attn(const moe_attn_shape* shape, int32_t n_seqs, int32_
 }
 
 struct AttnLayout {
-  size_t ctrl, seqs, hdr, units, recs, part_o, part_ml, total;
+  size_t ctrl, seqs, hdr, units, recs, done, part_o, part_ml, total;
   int PT, BP, rows_slot;
   bool few;
 };
@@ -1167,6 +1246,7 @@ static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, in
   const size_t slots = attn_may_cut(max_kv) ? kAttnMaxSlots : 0;
   W.units = take(sizeof(AttnUnit) * (blocks + slots));
   W.recs = take(sizeof(AttnRec) * std::min(blocks, slots / 2));
+  W.done = take(W.few ? sizeof(int) * 2 * slots * shape->n_kv_heads : 0);
   W.part_o = take(sizeof(float) * slots * W.rows_slot * shape->d);
   W.part_ml = take(sizeof(float2) * slots * W.rows_slot);
   W.total = (size_t)round_up((int64_t)pos, kAlign);
@@ -1231,6 +1311,7 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   a.hdr = reinterpret_cast<AttnHdr*>(w + W.hdr);
   a.units = reinterpret_cast<AttnUnit*>(w + W.units);
   a.recs = reinterpret_cast<AttnRec*>(w + W.recs);
+  a.done = reinterpret_cast<int*>(w + W.done);
   a.part_o = reinterpret_cast<float*>(w + W.part_o);
   a.part_ml = reinterpret_cast<float2*>(w + W.part_ml);
   const cudaError_t e = launch_attn(a, W.few, q, k, v, static_cast<cudaStream_t>(stream));
