@@ -75,9 +75,9 @@ struct GdnTP {
   float wd[kGdnChunk];               // e^{G_64 - G_i} / |k_i|, over `wd_scale`
   float keep;                        // e^{G_64}
   float t_scale, p_scale, wd_scale;  // what t, p and wd are to be multiplied by (powers of two but p's)
-  float pad[28];
+  float pad[60];
 };
-static_assert(sizeof(GdnTP) % 128 == 0, "bulk copies and alignment");
+static_assert(sizeof(GdnTP) % 256 == 0, "bulk copies; V behind it starts on a period of its swizzle");
 // Block of token tile t (8 tokens) and step k (16 tokens), k <= t / 2
 __host__ __device__ constexpr int gdn_block(int t, int k) { return (t / 2) * (t / 2 + 1) + (t & 1) * (t / 2 + 1) + k; }
 static_assert(gdn_block(7, 3) == GdnTP::kBlocks - 1, "lower triangle");
@@ -101,6 +101,7 @@ struct GdnPrefillArgs {
   GdnChunk* chunks;
   uint8_t* img;          // [chunk][Hk]: fp16 K then Q, 64 x dk each, rows' 16-byte pieces XORed with row & 7
   GdnTP* tp;             // [chunk][Hv]
+  alignas(64) CUtensorMap map_v;  // v: boxes of a slab's 16 values x 64 tokens (d_v % 8 == 0)
 };
 
 namespace {
@@ -598,7 +599,7 @@ struct GdnScanSmem {
   static constexpr int stage(int slabs) { return kV + slabs * kVSlab; }
   // exchange: per slab and warp, 8 tiles of S k and 8 of S q
   static constexpr int kXch = kWarps > 1 ? kWarps * 16 * 512 : 0;
-  static constexpr int bytes(int slabs) { return 2 * stage(slabs) + slabs * kXch; }
+  static constexpr int bytes(int slabs) { return 2 * stage(slabs) + slabs * kXch + 256; }
 };
 
 __device__ __forceinline__ void slab_sync(int slab, int threads) {
@@ -607,18 +608,19 @@ __device__ __forceinline__ void slab_sync(int slab, int threads) {
 __device__ __forceinline__ float4 cat(const float2 (&d)[2]) { return make_float4(d[0].x, d[0].y, d[1].x, d[1].y); }
 
 template <int DK, int NS>
-__global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
+__global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPrefillArgs a) {
   using M = GdnScanSmem<DK, NS>;
   constexpr int NW = M::kWarps;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[2];
+  uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slab = warp / NW, w = warp - slab * NW;
   const int g = lane >> 2, u = 2 * (lane & 3);
   const int stage_bytes = M::stage(a.slabs);
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1 + blockDim.x);
+    for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -644,24 +646,25 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
       if (a.S_in && vr + 8 * e < a.dv) S[t][e] = *reinterpret_cast<const float2*>(a.S_in + s_at + 8 * e * DK + t * 8);
     }
 
-  const bool v_wide = a.dv % 8 == 0;
-  auto load = [&](int c) {  // chunk c into its stage; every thread arrives on the stage's barrier
+  const bool v_tma = a.dv % 8 == 0;  // a copy's strides are multiples of 16 bytes
+  auto load = [&](int c) {  // chunk c into its stage
     uint8_t* st = smem + (c & 1) * stage_bytes;
     const size_t ch = (size_t)seq.chunk0 + c;
+    const int row0 = seq.row0 + c * kGdnChunk;
     if (tid == 0) {
-      mbar_expect_tx(&full[c & 1], M::kV);
+      mbar_expect_tx(&full[c & 1], M::kV + (v_tma ? a.slabs * M::kVSlab : 0));
       bulk_g2s(st, a.img + (ch * a.Hk + kh) * 2 * M::kImg, 2 * M::kImg, &full[c & 1]);
       bulk_g2s(st + M::kTp, a.tp + ch * a.Hv + h, sizeof(GdnTP), &full[c & 1]);
+      if (v_tma)  // values behind d_v and rows behind T are zeros, rows of the next sequence are cleared below
+        for (int x = 0; x < a.slabs; ++x)
+          tma_3d(smem_u32(st + M::kV + x * M::kVSlab), &a.map_v, v0 + x * kGdnSlab, h, row0, &full[c & 1]);
     }
-    const int row0 = seq.row0 + c * kGdnChunk, n = min(kGdnChunk, seq.n - c * kGdnChunk);
-    // V: per slab, token and half (8 values)
-    for (int i = tid; i < a.slabs * kGdnChunk * 2; i += blockDim.x) {
-      const int half = i % (2 * a.slabs), r = i / (2 * a.slabs), col = v0 + half * 8;
-      uint8_t* dst = st + M::kV + (half >> 1) * M::kVSlab + r * 32 + (((half & 1) ^ ((r >> 2) & 1)) << 4);
-      const uint16_t* src = a.v + ((size_t)(row0 + r) * a.Hv + h) * a.dv + col;
-      if (v_wide && r < n && col < a.dv) {
-        cp_async16(dst, src);
-      } else {
+    if (!v_tma) {
+      const int n = min(kGdnChunk, seq.n - c * kGdnChunk);
+      for (int i = tid; i < a.slabs * kGdnChunk * 2; i += blockDim.x) {  // per slab, token and half (8 values)
+        const int half = i % (2 * a.slabs), r = i / (2 * a.slabs), col = v0 + half * 8;
+        uint8_t* dst = st + M::kV + (half >> 1) * M::kVSlab + r * 32 + (((half & 1) ^ ((r >> 2) & 1)) << 4);
+        const uint16_t* src = a.v + ((size_t)(row0 + r) * a.Hv + h) * a.dv + col;
         uint32_t x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -671,7 +674,6 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
-    cp_async_arrive(&full[c & 1]);
   };
 
   // byte offsets of this lane's operand rows (the pieces' XOR depends on the lane alone)
@@ -793,6 +795,16 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const GdnPrefillArgs a) {
         for (int e = 0; e < 2; ++e)
           X[t + y][e] = ffma2(xa, X[t + y][e], make_float2(bf_lo(r[2 * y + e]), bf_hi(r[2 * y + e])));
       }
+    }
+    if (v_tma && seq.n - c * kGdnChunk < kGdnChunk) {  // tokens behind the sequence: V's rows are another's
+      const int n = seq.n - c * kGdnChunk;
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (t * 8 + u >= n) X[t][e].x = 0.f;
+          if (t * 8 + u + 1 >= n) X[t][e].y = 0.f;
+        }
     }
     // ---- W^T = R^T T'^T, left as W 2^k (W = fw * what is held) ----
     float2 W[8][2];
@@ -950,6 +962,13 @@ template <int DK>
 static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
   cudaError_t e = launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
+  if (a.T > 0 && a.dv % 8 == 0) {
+    const cuuint64_t dims[3] = {(cuuint64_t)a.dv, (cuuint64_t)a.Hv, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.dv * 2, (cuuint64_t)a.Hv * a.dv * 2};
+    const cuuint32_t box[3] = {kGdnSlab, 1, kGdnChunk};
+    e = encode_map(&a.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_32B);
+    if (e != cudaSuccess) return e;
+  }
   const long long chunks = (long long)a.T / kGdnChunk + std::min(a.n_seqs, a.T);
   if (chunks > 0) {
     e = cudaFuncSetAttribute(k_gdn_chunk<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, GdnChunkSmem<DK>::kBytes);
@@ -1055,7 +1074,7 @@ extern "C" moe_status moe_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs
                    beta, static_cast<uint16_t*>(out), 1, reinterpret_cast<Ctrl*>(w + W.ctrl),
                    reinterpret_cast<GdnHdr*>(w + W.hdr), reinterpret_cast<GdnSeq*>(w + W.seqs),
                    reinterpret_cast<int32_t*>(w + W.order), reinterpret_cast<GdnChunk*>(w + W.chunks), w + W.img,
-                   reinterpret_cast<GdnTP*>(w + W.tp)};
+                   reinterpret_cast<GdnTP*>(w + W.tp), {}};
   const cudaError_t e = launch_gdn_prefill(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gated delta prompt launch");
   return MOE_OK;
