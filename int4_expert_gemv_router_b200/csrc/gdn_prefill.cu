@@ -61,6 +61,7 @@ struct GdnChunk {
 };
 struct GdnHdr {
   int n_chunks;
+  int chain;  // the longest sequence is the critical path of the scan
 };
 
 // What k_gdn_chunk leaves for one chunk and value head.  T' and P as B operands of
@@ -94,6 +95,7 @@ struct GdnPrefillArgs {
   const float* beta;     // [T, Hv]
   uint16_t* out;         // bf16 [T, Hv, dv]
   int slabs;             // slabs of a scan CTA
+  int n_sm;
   Ctrl* ctrl;
   GdnHdr* hdr;
   GdnSeq* seqs;          // [n_seqs]
@@ -109,10 +111,12 @@ namespace {
 __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs a) {
   __shared__ int sh[32];
   __shared__ int bins[kPlanThreads];
+  __shared__ int s_longest;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
   bins[tid] = 0;
+  if (tid == 0) s_longest = 0;
   int seen = 0, chunks = 0;
   for (int base = 0; base < a.n_seqs; base += kPlanThreads) {
     const int i = base + tid;
@@ -124,10 +128,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs 
     const int c0 = block_excl_sum(nc, chunks, sh);
     if (!in) continue;
     a.seqs[i] = GdnSeq{r0, ok ? r1 - r0 : -1, c0};
+    if (ok) atomicMax(&s_longest, nc);
     if (!ok) atomicOr(&a.ctrl->err, kErrBadRange);
   }
-  if (tid == 0) a.hdr->n_chunks = chunks;
   __syncthreads();
+  if (tid == 0) {
+    a.hdr->n_chunks = chunks;
+    // Two slices a warp take less work, one a shorter time per chunk (6.5 against 4.5 us with all of
+    // an SM's warps at work): one where the longest sequence's chunks would take longer than all
+    // chunks spread over the SMs (lengths 1 to 1,531, ten sequences: 209 -> 180 us; four of 1,024:
+    // 191 against 159, so two there).
+    a.hdr->chain = (float)s_longest * a.n_sm > 1.2f * chunks * a.Hv * ((a.dv + 127) / 128);
+  }
   for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
     const GdnSeq q = a.seqs[s];
     for (int c = lane; c * kGdnChunk < q.n; c += 32)
@@ -609,32 +621,19 @@ __device__ __forceinline__ void slab_sync(int slab, int threads) {
 }
 __device__ __forceinline__ float4 cat(const float2 (&d)[2]) { return make_float4(d[0].x, d[0].y, d[1].x, d[1].y); }
 
+// One CTA's slabs of one sequence and value head: state rows rb * slabs * 16 and on.
 template <int DK, int NS>
-__global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPrefillArgs a) {
+__device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slabs, const GdnSeq seq, int s, int h, int rb,
+                                         uint8_t* smem, uint64_t* full) {
   using M = GdnScanSmem<DK, NS>;
   constexpr int NW = M::kWarps;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[2];
-  uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slab = warp / NW, w = warp - slab * NW;
   const int g = lane >> 2, u = 2 * (lane & 3);
-  const int stage_bytes = M::stage(a.slabs);
-  pdl_launch_dependents();
-  if (tid == 0) {
-    for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-  pdl_wait();
-  const int blocks = (a.dv + kGdnSlab * a.slabs - 1) / (kGdnSlab * a.slabs);
-  const int per = a.Hv * blocks;
-  const int s = a.order[blockIdx.x / per], rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
+  const int stage_bytes = M::stage(slabs);
   const int kh = h / (a.Hv / a.Hk);
-  const GdnSeq seq = a.seqs[s];
-  if (seq.n < 0) return;
   const int n_ch = (seq.n + kGdnChunk - 1) / kGdnChunk;
-  const int v0 = rb * a.slabs * kGdnSlab;       // first state row of the CTA
+  const int v0 = rb * slabs * kGdnSlab;       // first state row of the CTA
   const int vr = v0 + slab * kGdnSlab + g;      // this lane's rows: vr and vr + 8
   const size_t state = (size_t)s * a.Hv + h;
   const size_t s_at = (state * a.dv + vr) * DK + w * NS * kGdnSlice + u;  // this lane's first element
@@ -654,17 +653,17 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPre
     const size_t ch = (size_t)seq.chunk0 + c;
     const int row0 = seq.row0 + c * kGdnChunk;
     if (tid == 0) {
-      mbar_expect_tx(&full[c & 1], M::kV + (v_tma ? a.slabs * M::kVSlab : 0));
+      mbar_expect_tx(&full[c & 1], M::kV + (v_tma ? slabs * M::kVSlab : 0));
       bulk_g2s(st, a.img + (ch * a.Hk + kh) * 2 * M::kImg, 2 * M::kImg, &full[c & 1]);
       bulk_g2s(st + M::kTp, a.tp + ch * a.Hv + h, sizeof(GdnTP), &full[c & 1]);
       if (v_tma)  // values behind d_v and rows behind T are zeros, rows of the next sequence are cleared below
-        for (int x = 0; x < a.slabs; ++x)
+        for (int x = 0; x < slabs; ++x)
           tma_3d(smem_u32(st + M::kV + x * M::kVSlab), &a.map_v, v0 + x * kGdnSlab, h, row0, &full[c & 1]);
     }
     if (!v_tma) {
       const int n = min(kGdnChunk, seq.n - c * kGdnChunk);
-      for (int i = tid; i < a.slabs * kGdnChunk * 2; i += blockDim.x) {  // per slab, token and half (8 values)
-        const int half = i % (2 * a.slabs), r = i / (2 * a.slabs), col = v0 + half * 8;
+      for (int i = tid; i < slabs * kGdnChunk * 2; i += blockDim.x) {  // per slab, token and half (8 values)
+        const int half = i % (2 * slabs), r = i / (2 * slabs), col = v0 + half * 8;
         uint8_t* dst = st + M::kV + (half >> 1) * M::kVSlab + r * 32 + (((half & 1) ^ ((r >> 2) & 1)) << 4);
         const uint16_t* src = a.v + ((size_t)(row0 + r) * a.Hv + h) * a.dv + col;
         uint32_t x[4];
@@ -940,24 +939,60 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPre
       if (vr + 8 * e < a.dv) *reinterpret_cast<float2*>(a.S_out + s_at + 8 * e * DK + t * 8) = S[t][e];
 }
 
+// NS = 0: one slice a warp and 64 rows a CTA, or two slices and 128 rows, as the plan says; the grid
+// is the former's, so that every other CTA of the latter leaves.
+template <int DK, int NS>
+__global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPrefillArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[2];
+  uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  const int blocks = (a.dv + kGdnSlab * a.slabs - 1) / (kGdnSlab * a.slabs), per = a.Hv * blocks;
+  const int s = a.order[blockIdx.x / per], rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
+  const GdnSeq seq = a.seqs[s];
+  if (seq.n < 0) return;
+  if constexpr (NS > 0) {
+    gdn_scan<DK, NS>(a, a.slabs, seq, s, h, rb, smem, full);
+  } else if (a.hdr->chain) {
+    gdn_scan<DK, 1>(a, a.slabs, seq, s, h, rb, smem, full);
+  } else if (rb % 2 == 0) {
+    gdn_scan<DK, 2>(a, 2 * a.slabs, seq, s, h, rb / 2, smem, full);
+  }
+}
+
 }  // namespace
 
 // Slabs of a scan CTA: as many as shared memory holds (they share a chunk's K, Q, T' and P), but
-// no more than leave every SM a CTA.
+// no more than leave every SM a CTA.  NS = 0: 64 rows, and 128 for the sequences of two slices.
 template <int DK, int NS>
 static cudaError_t launch_gdn_scan(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
-  using M = GdnScanSmem<DK, NS>;
-  const int most = DK == 256 ? NS : DK == 128 ? 4 * NS : 8;
+  using M = GdnScanSmem<DK, NS ? NS : 1>;
   const long long heads = (long long)a.n_seqs * a.Hv;
-  a.slabs = 1;
-  while (a.slabs < most && heads * ((a.dv + 2 * kGdnSlab * a.slabs - 1) / (2 * kGdnSlab * a.slabs)) * 2 > n_sm &&
-         a.slabs * kGdnSlab < a.dv)
-    a.slabs *= 2;
+  int bytes, threads;
+  if constexpr (NS > 0) {
+    const int most = DK == 256 ? NS : DK == 128 ? 4 : 8;
+    a.slabs = 1;
+    while (a.slabs < most && heads * ((a.dv + 2 * kGdnSlab * a.slabs - 1) / (2 * kGdnSlab * a.slabs)) * 2 > n_sm &&
+           a.slabs * kGdnSlab < a.dv)
+      a.slabs *= 2;
+    bytes = M::bytes(a.slabs);
+    threads = a.slabs * M::kWarps * 32;
+  } else {
+    a.slabs = 4;
+    bytes = std::max(M::bytes(4), GdnScanSmem<DK, 2>::bytes(8));
+    threads = 256;
+  }
   const int rows = kGdnSlab * a.slabs;
-  const cudaError_t e = cudaFuncSetAttribute(k_gdn_scan<DK, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::bytes(a.slabs));
+  const cudaError_t e = cudaFuncSetAttribute(k_gdn_scan<DK, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_gdn_scan<DK, NS>, dim3((unsigned)(heads * ((a.dv + rows - 1) / rows))), dim3(a.slabs * M::kWarps * 32),
-                    M::bytes(a.slabs), s, a);
+  return launch_pdl(k_gdn_scan<DK, NS>, dim3((unsigned)(heads * ((a.dv + rows - 1) / rows))), dim3((unsigned)threads),
+                    (size_t)bytes, s, a);
 }
 
 template <int DK>
@@ -983,7 +1018,7 @@ static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream
   }
   if constexpr (DK > kGdnSlice) {
     const long long slabs = (long long)a.n_seqs * a.Hv * ((a.dv + kGdnSlab - 1) / kGdnSlab);
-    if (slabs >= 4LL * n_sm) return launch_gdn_scan<DK, 2>(a, n_sm, s);
+    if (slabs >= 4LL * n_sm) return launch_gdn_scan<DK, DK == 128 ? 0 : 2>(a, n_sm, s);
   }
   return launch_gdn_scan<DK, 1>(a, n_sm, s);
 }
@@ -993,6 +1028,7 @@ cudaError_t launch_gdn_prefill(GdnPrefillArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  a.n_sm = n_sm;
   switch (a.dk) {
     case 64: return launch_gdn_prefill_dk<64>(a, n_sm, s);
     case 128: return launch_gdn_prefill_dk<128>(a, n_sm, s);
@@ -1076,7 +1112,7 @@ extern "C" moe_status moe_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs
   uint8_t* w = static_cast<uint8_t*>(ws);
   GdnPrefillArgs a{n_seqs, T, shape->n_k_heads, shape->n_v_heads, shape->d_k, shape->d_v, offsets, state_in, state_out,
                    static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), g,
-                   beta, static_cast<uint16_t*>(out), 1, reinterpret_cast<Ctrl*>(w + W.ctrl),
+                   beta, static_cast<uint16_t*>(out), 1, 1, reinterpret_cast<Ctrl*>(w + W.ctrl),
                    reinterpret_cast<GdnHdr*>(w + W.hdr), reinterpret_cast<GdnSeq*>(w + W.seqs),
                    reinterpret_cast<int32_t*>(w + W.order), reinterpret_cast<GdnChunk*>(w + W.chunks), w + W.img,
                    reinterpret_cast<GdnTP*>(w + W.tp), {}};
