@@ -352,10 +352,10 @@ __device__ __forceinline__ void invert(float* L, int t, int team) {
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArgs a) {
+__global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(const GdnPrefillArgs a) {
   using M = GdnChunkSmem<DK>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk];
+  __shared__ float s_up[2 * kGdnChunk], s_ck[kGdnChunk], s_cq[kGdnChunk], s_beta[2][kGdnChunk];
   __shared__ float2 s_G[2][kGdnChunk];  // log2(e) G_i, as two floats
   __shared__ float s_pm[2];             // the largest G_i - G_j, j <= i (0 where nothing grows)
   __shared__ float s_red[2][6];
@@ -381,43 +381,58 @@ __global__ void __launch_bounds__(kChunkThreads) k_gdn_chunk(const GdnPrefillArg
     uint4* dst = reinterpret_cast<uint4*>(a.img + ((size_t)chunk * a.Hk + kh) * 2 * M::kImg);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int x = i * kChunkThreads + tid, r = x / LPR, col = x % LPR, z = r >> 6, row = r & 63;
+      const int r = i * (kChunkThreads / LPR) + tid / LPR, row = r & 63;  // K, then Q
       piece[i] = make_uint4(0, 0, 0, 0);
       if (row < C.n)
-        piece[i] = *reinterpret_cast<const uint4*>((z ? a.q : a.k) + ((size_t)(C.row0 + row) * a.Hk + kh) * DK + col * 8);
+        piece[i] = *reinterpret_cast<const uint4*>((i >= N / 2 ? a.q : a.k) + ((size_t)(C.row0 + row) * a.Hk + kh) * DK + tid % LPR * 8);
     }
+    // the rows' sums of squares side by side, then their scales, then the values
+    float ss[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int x = i * kChunkThreads + tid, r = x / LPR, col = x % LPR, z = r >> 6, row = r & 63;
-      float v[8], ss = 0.f;
+      ss[i] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t w = word_of(piece[i], e);
-        v[2 * e] = bf_lo(w);
-        v[2 * e + 1] = bf_hi(w);
-        ss = fmaf(v[2 * e], v[2 * e], fmaf(v[2 * e + 1], v[2 * e + 1], ss));
+        ss[i] = fmaf(bf_lo(w), bf_lo(w), fmaf(bf_hi(w), bf_hi(w), ss[i]));
       }
+    }
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float norm = sqrtf(ss);
+    for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+    const int col = tid % LPR;
+    if (col == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s_up[i * (kChunkThreads / LPR) + tid / LPR] = ss[i];
+    __syncthreads();
+    if (tid < 2 * kGdnChunk) {  // a thread a row
+      const float norm = sqrtf(s_up[tid]);
       // 2^e2 brings the norm to [2^10, 2^11).  A row of a norm below 2^-100 (it vanishes next to
       // 1e-6), and one whose sum of squares overflows (1 / inf), is 0; infinities and NaN give NaN.
       const int ne = (int)(__float_as_uint(norm) >> 23) - 127;
       const bool zero = ne <= -100 || ne == 128;
-      const float up = zero ? 0.f : __uint_as_float((uint32_t)(137 - ne) << 23);
       const float down = zero ? 0.f : __uint_as_float((uint32_t)(117 + ne) << 23);
-      if (col == 0) {
-        const float c = zero ? 0.f : down / fmaxf(norm, 1e-6f);  // the normalised row is c times the stored one
-        if (z) s_cq[row] = c * rsqrtf((float)DK);
-        else s_ck[row] = c;
-      }
-      uint32_t hv[4];
+      const float c = zero ? 0.f : down / fmaxf(norm, 1e-6f);  // the normalised row is c times the stored one
+      s_up[tid] = zero ? 0.f : __uint_as_float((uint32_t)(137 - ne) << 23);
+      if (tid < kGdnChunk) s_ck[tid] = c;
+      else s_cq[tid - kGdnChunk] = c * rsqrtf((float)DK);
+    }
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hv[e] = pack_h2(make_float2(v[2 * e] * up, v[2 * e + 1] * up));
-      const uint4 h = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+    for (int i = 0; i < N; ++i) {
+      const int r = i * (kChunkThreads / LPR) + tid / LPR, row = r & 63;
+      const float up = s_up[r];
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = word_of(piece[i], e);
+        h[e] = pack_h2(mul2(make_float2(bf_lo(w), bf_hi(w)), both(up)));
+      }
       const int at = r * LPR + (col ^ (row & 7));
-      reinterpret_cast<uint4*>(smem)[at] = h;
-      dst[at] = h;
+      const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]);
+      reinterpret_cast<uint4*>(smem)[at] = hv;
+      dst[at] = hv;
     }
   }
   // Decays: sums in 64 bits (their differences have to be good to 24; a forgotten state's g is
