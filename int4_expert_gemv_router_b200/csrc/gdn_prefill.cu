@@ -767,33 +767,28 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
           Y[t][e] = mul2(Y[t][e], both(dn[e]));
         }
     }
-    // ---- sums over the slab's warps (each the same, in the same order); of Y only the tiles
-    // t % NW == w that this warp finishes ----
+    // ---- sums over the slab's warps, each the same in the same order: of X here, of Y at the output,
+    // where a warp finishes the tiles t % NW == w ----
+    float4* xch = reinterpret_cast<float4*>(smem + 2 * stage_bytes + slab * M::kXch);
     if constexpr (NW > 1) {
-      float4* xch = reinterpret_cast<float4*>(smem + 2 * stage_bytes + slab * M::kXch);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         xch[(w * 16 + t) * 32 + lane] = cat(X[t]);
-        if (NW > 2 || t % NW != w) xch[(w * 16 + 8 + t) * 32 + lane] = cat(Y[t]);
+        xch[(w * 16 + 8 + t) * 32 + lane] = cat(Y[t]);
       }
       slab_sync(slab, NW * 32);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
+        if constexpr (NW == 2) {  // the sum of two is the same either way
+          const float4 x = xch[((1 - w) * 16 + t) * 32 + lane];
+          X[t][0] = add2(X[t][0], make_float2(x.x, x.y));
+          X[t][1] = add2(X[t][1], make_float2(x.z, x.w));
+        } else {
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          if (z && t % NW != w) continue;
-          float2 (&D)[2] = z ? Y[t] : X[t];
-          if constexpr (NW == 2) {  // the sum of two is the same either way
-            const float4 x = xch[((1 - w) * 16 + z * 8 + t) * 32 + lane];
-            D[0] = add2(D[0], make_float2(x.x, x.y));
-            D[1] = add2(D[1], make_float2(x.z, x.w));
-          } else {
-#pragma unroll
-            for (int v = 0; v < NW; ++v) {
-              const float4 x = xch[(v * 16 + z * 8 + t) * 32 + lane];
-              D[0] = v ? add2(D[0], make_float2(x.x, x.y)) : make_float2(x.x, x.y);
-              D[1] = v ? add2(D[1], make_float2(x.z, x.w)) : make_float2(x.z, x.w);
-            }
+          for (int v = 0; v < NW; ++v) {
+            const float4 x = xch[(v * 16 + t) * 32 + lane];
+            X[t][0] = v ? add2(X[t][0], make_float2(x.x, x.y)) : make_float2(x.x, x.y);
+            X[t][1] = v ? add2(X[t][1], make_float2(x.z, x.w)) : make_float2(x.z, x.w);
           }
         }
       }
@@ -874,33 +869,55 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
       const float ps = tp->p_scale, f0 = fw[0] * ps, f1 = fw[1] * ps;
       uint16_t* out = a.out + ((size_t)(seq.row0 + c * kGdnChunk) * a.Hv + h) * a.dv;
       const size_t tok_stride = (size_t)a.Hv * a.dv;
+      // tiles t = i NW + w, their products side by side
+      constexpr int NO = 8 / NW;
+      float2 o[NO][2];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t % NW != w) continue;
-        float2 o[2];
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k <= t / 2; ++k) {
-          const uint2 b = tp->p[gdn_block(t, k)][lane];
-          if (k == 0) mma16z(o, hi[0][0], hi[0][1], hi[1][0], hi[1][1], b.x, b.y);
-          else mma16(o, hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b.x, b.y);
+        for (int i = 0; i < NO; ++i) {
+          // steps k <= t / 2; with NW = 4 that is 2 i + w / 2, and the step 2 i + 1 of the first two
+          // warps reads another block and is not added
+          if (k > (i * NW + NW - 1) / 2) continue;
+          const int t = i * NW + w;
+          const bool in = NW < 4 || k <= t / 2;
+          uint2 b = tp->p[in ? gdn_block(t, k) : 0][lane];
+          if (!in) b = make_uint2(0, 0);
+          if (k == 0) mma16z(o[i], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b.x, b.y);
+          else mma16(o[i], hi[2 * k][0], hi[2 * k][1], hi[2 * k + 1][0], hi[2 * k + 1][1], b.x, b.y);
         }
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        const int t = i * NW + w;
         const float2 oa = *reinterpret_cast<const float2*>(&tp->oa[t * 8 + u]);
-        o[0] = ffma2(oa, Y[t][0], mul2(o[0], both(f0)));
-        o[1] = ffma2(oa, Y[t][1], mul2(o[1], both(f1)));
+        float2 y[2];
+        if constexpr (NW == 1) {
+          y[0] = Y[i][0];
+          y[1] = Y[i][1];
+        } else {
+#pragma unroll
+          for (int v = 0; v < NW; ++v) {
+            const float4 x = xch[(v * 16 + 8 + t) * 32 + lane];
+            y[0] = v ? add2(y[0], make_float2(x.x, x.y)) : make_float2(x.x, x.y);
+            y[1] = v ? add2(y[1], make_float2(x.z, x.w)) : make_float2(x.z, x.w);
+          }
+        }
+        o[i][0] = ffma2(oa, y[0], mul2(o[i][0], both(f0)));
+        o[i][1] = ffma2(oa, y[1], mul2(o[i][1], both(f1)));
         if (a.dv % 2 == 0) {
           // pairs of columns: lanes of even g take the token u of rows g, g + 1, odd ones u + 1
           const int odd = g & 1, tok = t * 8 + u + odd, col = vr - odd;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[e].x : o[e].y, 4);
-            const uint32_t v = odd ? pack_bf16(got, o[e].y) : pack_bf16(o[e].x, got);
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i][e].x : o[i][e].y, 4);
+            const uint32_t v = odd ? pack_bf16(got, o[i][e].y) : pack_bf16(o[i][e].x, got);
             if (tok < n && col + 8 * e < a.dv) *reinterpret_cast<uint32_t*>(out + tok * tok_stride + col + 8 * e) = v;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = t * 8 + u + (e & 1), col = vr + 8 * (e >> 1);
-            if (tok < n && col < a.dv) out[tok * tok_stride + col] = f2bf(e & 1 ? o[e >> 1].y : o[e >> 1].x);
+            if (tok < n && col < a.dv) out[tok * tok_stride + col] = f2bf(e & 1 ? o[i][e >> 1].y : o[i][e >> 1].x);
           }
         }
       }
