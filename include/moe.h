@@ -371,11 +371,13 @@ MOE_API moe_status moe_gdn_decode_step_ex(const moe_gdn_shape* shape, int32_t B,
  *   beta       (dev) fp32 [T, H_v]
  *   out        (dev) bf16 [T, H_v, d_v] (round to nearest even of the fp32 value)
  *   ws         (dev) workspace of ws_bytes >= moe_gdn_prefill_workspace_size(shape, n_seqs, T)
- * Shapes as moe_gdn_decode_step.  Rows of out that belong to no sequence are left as they
+ * Shapes as moe_gdn_decode_step.  The workspace holds what each 64-token chunk needs, about
+ * 4 d_k H_k + 270 H_v bytes per token.  Rows of out that belong to no sequence are left as they
  * were.  A sequence whose range is out of order or outside [0, T] (offsets[s+1] < offsets[s],
  * offsets[s+1] > T, or offsets[s] below an earlier offset) is left out, its rows of out and
- * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  Deterministic: the same inputs
- * give the same bits, whatever the other sequences of the call are.
+ * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  An infinity or NaN in a token's
+ * inputs reaches the tokens behind it, and may reach those before it in its chunk of 64 tokens.
+ * Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_gdn_prefill_workspace_size(const moe_gdn_shape* shape, int32_t n_seqs, int32_t T,
                                                   size_t* bytes);
@@ -421,7 +423,7 @@ typedef struct {
  * keys lie outside [0, kv_rows) or number more than max_kv, is left out, its rows of out
  * untouched, and MOE_DEVERR_BAD_RANGE is set.  Sequences may share keys.  A key's value of
  * infinity or NaN reaches the queries that see it, and may reach queries before it within 128
- * keys of it.  Deterministic: the same inputs and the same call sizes give the same bits.
+ * keys of it.  Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_attn_workspace_size(const moe_attn_shape* shape, int32_t n_seqs, int32_t T, int32_t max_kv,
                                            size_t* bytes);

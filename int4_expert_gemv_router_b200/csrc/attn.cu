@@ -28,8 +28,8 @@
 //                   tokens): units of 16 rows on mma.sync, see there
 //   k_attn_join     joins the pieces of blocks that k_attn had cut
 //
-// What is rounded: P to bf16 (the tensor core's operand; one half step, 2^-8, of each weight),
-// and the result.  S, O, m and the sums are fp32.  A maximum may lag the true one by up to 2^8:
+// What is rounded: P to bf16 (the tensor core's operand; one half step, 2^-8, of each weight; with
+// few rows, where the tensor core has time, to two bf16 values, 2^-16), and the result.  S, O, m and the sums are fp32.  A maximum may lag the true one by up to 2^8:
 // P keeps its relative precision and the fp32 sums their range.
 #include "../../include/moe.h"
 #include "common.cuh"
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kLoadWarp && lane < 3)
+  if (warp == kLoadWarp && lane < (a.kv_rows > 0 ? 3 : 1))
     prefetch_map(lane == 0 ? &a.map_q : lane == 1 ? &a.map_k : &a.map_v);
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   pdl_launch_dependents();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* sums = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + NS * 2 * L::kTile);
-  if (warp == kFewWarps && lane < 2) prefetch_map(lane ? &a.map_v : &a.map_k);
+  if (warp == kFewWarps && lane < 2 && a.kv_rows > 0) prefetch_map(lane ? &a.map_v : &a.map_k);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
           for (int i = 0; i < 4; ++i) O[n][i] *= f[i >> 1];
       }
       const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-      uint32_t p[4];
+      uint32_t p[4], pl[4];  // the weights and what their rounding to bf16 leaves
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const float p0 = ex2(x[n][0] - b0), p1 = ex2(x[n][1] - b0), p2 = ex2(x[n][2] - b1), p3 = ex2(x[n][3] - b1);
@@ -924,6 +924,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         l[1] += p2 + p3;
         p[2 * n] = pack_bf16(p0, p1);
         p[2 * n + 1] = pack_bf16(p2, p3);
+        pl[2 * n] = pack_bf16(p0 - bf_lo(p[2 * n]), p1 - bf_hi(p[2 * n]));
+        pl[2 * n + 1] = pack_bf16(p2 - bf_lo(p[2 * n + 1]), p3 - bf_hi(p[2 * n + 1]));
       }
       // Rows behind the sequence's last key hold anything, and 0 times an infinity or NaN is NaN: this
       // warp clears its own.
@@ -943,6 +945,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         ldsm4_t(tv + (n2 >> 2) * L::kBox + vrow * 128 + ((((n2 & 3) * 2 + (lane >> 4)) ^ (vrow & 7)) << 4), b);
         mma_bf16(O[2 * n2], p, b[0], b[1]);
         mma_bf16(O[2 * n2 + 1], p, b[2], b[3]);
+        mma_bf16(O[2 * n2], pl, b[0], b[1]);
+        mma_bf16(O[2 * n2 + 1], pl, b[2], b[3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);

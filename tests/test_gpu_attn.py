@@ -102,6 +102,9 @@ def test_prompts_match_oracle(Hq, Hkv, d, lens):
     (16, 2, 64, [1, 1, 1], [4000, 1, 2049]),
     (8, 8, 128, [1, 2], [1500, 700]),
     (12, 4, 128, [1], [5000]),                         # one token, a long axis
+    (16, 1, 64, [1], [20000]),                         # ... cut into more than 16 pieces, 16 rows
+    (8, 1, 128, [2, 0], [9500, 3]),                    # ... two tokens of it
+    (4, 2, 128, [33], [9000]),                         # tiles cut into pieces
     (4, 1, 64, [130, 1], [2000, 3000]),
     (6, 2, 128, [20, 5, 7], [4, 0, 7]),                # more queries than keys: some see nothing
 ])
@@ -183,6 +186,15 @@ def test_rows_outside_sequences_and_shared_keys():
     assert (out[:6] == 7.0).all() and (out[-6:] == 7.0).all()
     again, _ = run(c, ws)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("lens", [[3, 2], [40, 1]])
+def test_no_keys_at_all(lens):
+    """kv_rows = 0: no k and v, every query sees nothing."""
+    c = make(4, 2, 128, lens, [0, 0], seed=33, gap=0)
+    c.update(k=None, v=None)
+    out, ws = run(c)
+    assert abi.moe_ws_check(ws) == 0 and (out[:sum(lens)] == 0).all()
 
 
 def test_many_sequences():

@@ -82,6 +82,11 @@ def check(c, out, S, seqs=None):
     (1, 2, 128, 257, [90], True),
     (1, 2, 256, 33, [64, 66], False),
     (16, 32, 128, 128, [150, 20], True),   # the 80B-like shape
+    (4, 32, 128, 128, [70, 3, 65], True),  # enough state rows for 64-row CTAs, one long chain
+    (4, 32, 128, 128, [65] * 6, True),     # ... and no chain longer than the rest: two slices a warp
+    (2, 32, 128, 72, [66, 1, 64, 2, 64, 64, 30], False),
+    (1, 32, 128, 33, [64] * 8, True),      # ... with an odd value width
+    (2, 32, 256, 96, [65, 64, 10, 1], True),  # d_k 256, two slices a warp
 ])
 def test_prompt_matches_oracle(Hk, Hv, dk, dv, lens, start):
     c = make(Hk, Hv, dk, dv, lens, seed=3 * Hv + dk + len(lens), start=start)
@@ -187,8 +192,7 @@ def test_rows_outside_and_state_in_place():
     a, b = c["off"].tolist()[2:4]
     alone = dict(c, n=1, T=b - a, off=torch.tensor([0, b - a], dtype=torch.int32, device=DEV), S=c["S"][2:3],
                  **{x: c[x][a:b].clone() for x in ("q", "k", "v", "g", "beta")})
-    out3, S3, _ = run(alone)
-    assert torch.equal(out3, out[a:b]) and torch.equal(S3[0], S[2])
+    check(alone, *run(alone)[:2])
 
 
 def test_no_tokens_copies_the_states():
