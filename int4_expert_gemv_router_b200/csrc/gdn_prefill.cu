@@ -14,7 +14,7 @@
 // L needs no state, so everything but the products with S is done for all chunks at once:
 //
 //   k_gdn_plan   one CTA: checks the row ranges, lists the chunks, orders the sequences longest
-//                first (they are the critical path)
+//                first (they are the critical path); small calls of few sequences do without it
 //   k_gdn_chunk  a CTA per chunk and key head: norms, K K^T and Q K^T on the tensor cores, the
 //                decays, T' = (I + L)^-1 diag(beta) by block inversion and P = D o Q^ K^^T;
 //                leaves K, Q, T' and P in the operand layout of the next kernel
@@ -96,6 +96,7 @@ struct GdnPrefillArgs {
   uint16_t* out;         // bf16 [T, Hv, dv]
   int slabs;             // slabs of a scan CTA
   int n_sm;
+  int warp_plan;         // no plan kernel (see gdn_warp_plan)
   Ctrl* ctrl;
   GdnHdr* hdr;
   GdnSeq* seqs;          // [n_seqs]
@@ -107,6 +108,46 @@ struct GdnPrefillArgs {
 };
 
 namespace {
+
+// Calls of up to 32 sequences and 16 chunk CTAs an SM need no plan kernel: every warp of the other two
+// works the plan out for itself, a lane a sequence (17 tokens: 19.4 -> 16.9 us; but 16 x 1024 tokens,
+// 29 chunk CTAs an SM: 564 -> 574).
+constexpr int kWarpSeqs = 32;
+struct GdnWarpPlan {
+  GdnSeq seq;            // this lane's sequence (n < 0: left out, or none)
+  int nc, n_chunks;      // its chunks, the call's
+  bool bad;
+};
+__device__ __forceinline__ GdnWarpPlan gdn_warp_plan(const GdnPrefillArgs& a, int lane) {
+  const bool in = lane < a.n_seqs;
+  const int r0 = in ? a.offsets[lane] : 0, r1 = in ? a.offsets[lane + 1] : 0;
+  int seen = lane ? __shfl_up_sync(0xffffffffu, r0, 1) : (__shfl_up_sync(0xffffffffu, r0, 1), 0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, seen, o);
+    if (lane >= o) seen = max(seen, v);
+  }
+  GdnWarpPlan p;
+  const bool ok = in && rows_ok(r0, r1, max(seen, 0), a.T);
+  p.bad = in && !ok;
+  p.nc = ok ? (r1 - r0 + kGdnChunk - 1) / kGdnChunk : 0;
+  int sum = p.nc;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  p.n_chunks = __shfl_sync(0xffffffffu, sum, 31);
+  p.seq = GdnSeq{r0, ok ? r1 - r0 : -1, sum - p.nc};
+  return p;
+}
+// Two slices a warp take less work, one a shorter time per chunk (6.5 against 4.5 us with all of an
+// SM's warps at work): one where the longest sequence's chunks would take longer than all chunks
+// spread over the SMs (lengths 1 to 1,531, ten sequences: 209 -> 180 us; four of 1,024: 191 against
+// 159, so two there).
+__device__ __forceinline__ bool gdn_chain(const GdnPrefillArgs& a, int longest, int n_chunks) {
+  return (float)longest * a.n_sm > 1.2f * n_chunks * a.Hv * ((a.dv + 127) / 128);
+}
 
 __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs a) {
   __shared__ int sh[32];
@@ -134,11 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs 
   __syncthreads();
   if (tid == 0) {
     a.hdr->n_chunks = chunks;
-    // Two slices a warp take less work, one a shorter time per chunk (6.5 against 4.5 us with all of
-    // an SM's warps at work): one where the longest sequence's chunks would take longer than all
-    // chunks spread over the SMs (lengths 1 to 1,531, ten sequences: 209 -> 180 us; four of 1,024:
-    // 191 against 159, so two there).
-    a.hdr->chain = (float)s_longest * a.n_sm > 1.2f * chunks * a.Hv * ((a.dv + 127) / 128);
+    a.hdr->chain = gdn_chain(a, s_longest, chunks);
   }
   for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
     const GdnSeq q = a.seqs[s];
@@ -363,9 +400,18 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
   pdl_launch_dependents();
   pdl_wait();
   const int chunk = blockIdx.x / a.Hk, kh = blockIdx.x - chunk * a.Hk;
-  const int n_chunks = a.hdr->n_chunks;
-  const GdnChunk C = a.chunks[chunk];  // the grid is the table's size; behind n_chunks it holds anything
-  if (chunk >= n_chunks) return;
+  GdnChunk C;
+  if (a.warp_plan) {
+    const GdnWarpPlan p = gdn_warp_plan(a, lane);
+    if (chunk >= p.n_chunks) return;
+    const int at = chunk - p.seq.chunk0, src = __ffs(__ballot_sync(0xffffffffu, at >= 0 && at < p.nc)) - 1;
+    C.row0 = __shfl_sync(0xffffffffu, p.seq.row0 + at * kGdnChunk, src);
+    C.n = __shfl_sync(0xffffffffu, min(kGdnChunk, p.seq.n - at * kGdnChunk), src);
+  } else {
+    const int n_chunks = a.hdr->n_chunks;
+    C = a.chunks[chunk];  // the grid is the table's size; behind n_chunks it holds anything
+    if (chunk >= n_chunks) return;
+  }
   uint8_t* img[2] = {smem, smem + M::kImg};
   float* kk = reinterpret_cast<float*>(smem + M::kFirst);
   float* qk = kk + kGdnChunk * kMatLd;
@@ -986,12 +1032,32 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPre
   __syncthreads();
   pdl_wait();
   const int blocks = (a.dv + kGdnSlab * a.slabs - 1) / (kGdnSlab * a.slabs), per = a.Hv * blocks;
-  const int s = a.order[blockIdx.x / per], rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
-  const GdnSeq seq = a.seqs[s];
+  const int place = blockIdx.x / per, rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
+  int s;
+  GdnSeq seq;
+  bool chain;
+  if (a.warp_plan) {
+    const int lane = threadIdx.x & 31;
+    const GdnWarpPlan p = gdn_warp_plan(a, lane);
+    if (blockIdx.x == 0 && threadIdx.x < 32 && p.bad) atomicOr(&a.ctrl->err, kErrBadRange);
+    int longest = p.nc, rank = lane < a.n_seqs ? 0 : -1;  // longest first
+    for (int i = 0; i < a.n_seqs; ++i) {
+      const int nc = __shfl_sync(0xffffffffu, p.nc, i);
+      longest = max(longest, nc);
+      if (lane < a.n_seqs && (nc > p.nc || (nc == p.nc && i < lane))) ++rank;
+    }
+    s = __ffs(__ballot_sync(0xffffffffu, rank == place)) - 1;
+    seq = GdnSeq{__shfl_sync(0xffffffffu, p.seq.row0, s), __shfl_sync(0xffffffffu, p.seq.n, s), __shfl_sync(0xffffffffu, p.seq.chunk0, s)};
+    chain = gdn_chain(a, longest, p.n_chunks);
+  } else {
+    s = a.order[place];
+    seq = a.seqs[s];
+    chain = a.hdr->chain;
+  }
   if (seq.n < 0) return;
   if constexpr (NS > 0) {
     gdn_scan<DK, NS>(a, a.slabs, seq, s, h, rb, smem, full);
-  } else if (a.hdr->chain) {
+  } else if (chain) {
     gdn_scan<DK, 1>(a, a.slabs, seq, s, h, rb, smem, full);
   } else if (rb % 2 == 0) {
     gdn_scan<DK, 2>(a, 2 * a.slabs, seq, s, h, rb / 2, smem, full);
@@ -1029,7 +1095,10 @@ static cudaError_t launch_gdn_scan(GdnPrefillArgs& a, int n_sm, cudaStream_t s) 
 
 template <int DK>
 static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream_t s) {
-  cudaError_t e = launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
+  const long long chunks = (long long)a.T / kGdnChunk + std::min(a.n_seqs, a.T);
+  a.warp_plan = a.n_seqs <= kWarpSeqs && chunks * a.Hk <= 16LL * n_sm;
+  cudaError_t e = cudaSuccess;
+  if (!a.warp_plan) e = launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   if (a.T > 0 && a.dv % 8 == 0) {
     const cuuint64_t dims[3] = {(cuuint64_t)a.dv, (cuuint64_t)a.Hv, (cuuint64_t)a.T};
@@ -1038,7 +1107,6 @@ static cudaError_t launch_gdn_prefill_dk(GdnPrefillArgs& a, int n_sm, cudaStream
     e = encode_map(&a.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_32B);
     if (e != cudaSuccess) return e;
   }
-  const long long chunks = (long long)a.T / kGdnChunk + std::min(a.n_seqs, a.T);
   if (chunks > 0) {
     // A grid of up to two CTAs an SM asks for as much shared memory as keeps a third from joining
     // them on some SMs while others idle (1,000 tokens, 272 CTAs: 69 against 65 us).
@@ -1144,7 +1212,7 @@ extern "C" moe_status moe_gdn_prefill(const moe_gdn_shape* shape, int32_t n_seqs
   uint8_t* w = static_cast<uint8_t*>(ws);
   GdnPrefillArgs a{n_seqs, T, shape->n_k_heads, shape->n_v_heads, shape->d_k, shape->d_v, offsets, state_in, state_out,
                    static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), g,
-                   beta, static_cast<uint16_t*>(out), 1, 1, reinterpret_cast<Ctrl*>(w + W.ctrl),
+                   beta, static_cast<uint16_t*>(out), 1, 1, 0, reinterpret_cast<Ctrl*>(w + W.ctrl),
                    reinterpret_cast<GdnHdr*>(w + W.hdr), reinterpret_cast<GdnSeq*>(w + W.seqs),
                    reinterpret_cast<int32_t*>(w + W.order), reinterpret_cast<GdnChunk*>(w + W.chunks), w + W.img,
                    reinterpret_cast<GdnTP*>(w + W.tp), {}};
