@@ -64,6 +64,7 @@ struct alignas(16) AttnRec {  // a block cut into pieces
 };
 struct AttnHdr {
   int n_units, n_recs;
+  int ticket;  // units given out beyond each CTA's first
 };
 
 constexpr int kAttnTile = 128;     // rows of a query tile and of a key tile
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
   if (tid == 0) {
     a.hdr->n_units = bins[a.sort ? kPlanThreads - 1 : 0] * a.Hkv;
     a.hdr->n_recs = s_recs;
+    a.hdr->ticket = 0;
   }
 }
 
@@ -344,10 +346,52 @@ __device__ __forceinline__ uint32_t attn_idesc(int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Unit number of this CTA's it-th round: rounds alternate direction, so that the CTA with the
-// longest unit of one round gets the shortest of the next.
+// Unit number of this CTA's it-th round, where units are dealt out beforehand (few rows: a ticket costs
+// more than it evens out): rounds alternate direction, so that the CTA with the longest unit of one
+// round gets the shortest of the next.
 __device__ __forceinline__ int unit_index(int it) {
   return it * (int)gridDim.x + ((it & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+// Many rows: units are given out one by one, longest first: a CTA's first is its own number, later ones come from
+// the ticket counter.  (Dealt out in rounds beforehand, the longest CTA of the ragged prompts had 30
+// key tiles, the mean 25.)  The loading warp draws them and hands them to the CTA's other warps.
+struct UnitQueue {
+  uint64_t full[2], empty[2];
+  int unit[2];  // -1: no more
+};
+__device__ __forceinline__ void queue_init(UnitQueue& q, int readers) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&q.full[i], 1);
+    mbar_init(&q.empty[i], readers);
+  }
+}
+// The next unit, by the loading warp (it: units so far); -1 at the end.  False: a wait ran out.
+__device__ __forceinline__ bool queue_draw(UnitQueue& q, const AttnArgs& a, int it, int n_units, int lane, int& unit) {
+  if (!__all_sync(0xffffffffu, mbar_wait(&q.empty[it & 1], ((it >> 1) & 1) ^ 1) ? 1 : 0)) {
+    if (lane == 0) atomicOr(&a.ctrl->err, kErrTimeout);
+    return false;
+  }
+  int u = 0;
+  if (lane == 0) {
+    u = it ? (int)gridDim.x + atomicAdd(&a.hdr->ticket, 1) : (int)blockIdx.x;
+    if (u >= n_units) u = -1;
+    q.unit[it & 1] = u;
+    mbar_arrive(&q.full[it & 1]);
+  }
+  unit = __shfl_sync(0xffffffffu, u, 0);
+  return true;
+}
+// ... and by the others, a warp each.
+__device__ __forceinline__ bool queue_take(UnitQueue& q, const AttnArgs& a, int it, int lane, int& unit) {
+  if (!__all_sync(0xffffffffu, mbar_wait(&q.full[it & 1], (it >> 1) & 1) ? 1 : 0)) {
+    if (lane == 0) atomicOr(&a.ctrl->err, kErrTimeout);
+    return false;
+  }
+  unit = *reinterpret_cast<volatile int*>(&q.unit[it & 1]);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&q.empty[it & 1]);
+  return true;
 }
 
 // What every role derives from a unit: per tile (A: 0, B: 1) its positions and key tiles.
@@ -386,6 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2][2], p_full[2][2],
       o_prev[2], o_done[2], o_free[2], v_fix, drain[2];
+  __shared__ UnitQueue queue;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -410,6 +455,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       mbar_init(&o_free[x], 4);
     }
     mbar_init(&q_free, 2);
+    queue_init(queue, kSoftWarps + 2);
     mbar_init(&v_fix, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -439,9 +485,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     const float sl = fabsf(a.scale_log2);
     int n_s = 0, n_u = 0;  // key tiles and units (with key tiles) so far
     bool alive = true;
-    for (int it = 0; alive && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
-      int head;
-      const AttnWork w = attn_work(a, unit_index(it), head);
+    for (int it = 0; alive && !warp_aborted(&s_abort); ++it) {
+      int head, unit;
+      if (!queue_take(queue, a, it, lane, unit)) {
+        alive = false;
+        break;
+      }
+      if (unit < 0) break;
+      const AttnWork w = attn_work(a, unit, head);
       const int np = x ? w.np[1] : w.np[0], nk = x ? w.nk[1] : w.nk[0];
       if (np == 0) continue;
       const int seen_r = pos < np ? w.u.seen + x * a.PT + pos : 0;  // keys this row sees (a row in use or 0)
@@ -623,9 +674,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
       }
       umma_commit_if(&s_full[x][h], lead);
     };
-    for (int it = 0; ok && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
-      int head;
-      const AttnWork w = attn_work(a, unit_index(it), head);
+    for (int it = 0; ok && !warp_aborted(&s_abort); ++it) {
+      int head, unit;
+      if (!queue_take(queue, a, it, lane, unit)) {
+        ok = false;
+        break;
+      }
+      if (unit < 0) break;
+      const AttnWork w = attn_work(a, unit, head);
       if (w.n == 0) continue;
       const int nk = x ? w.nk[1] : w.nk[0];
       if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
@@ -675,9 +731,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
     int kv = 0, n_q[2] = {0, 0}, n_act = 0, n_fix = 0;
     bool ok = true;
     const uint32_t q_bytes = (uint32_t)a.PT * a.G * D * 2;
-    for (int it = 0; ok && unit_index(it) < n_units && !warp_aborted(&s_abort); ++it) {
-      int head;
-      const AttnWork w = attn_work(a, unit_index(it), head);
+    for (int it = 0; ok && !warp_aborted(&s_abort); ++it) {
+      int head, unit;
+      if (!queue_draw(queue, a, it, n_units, lane, unit)) {
+        ok = false;
+        break;
+      }
+      if (unit < 0) break;
+      const AttnWork w = attn_work(a, unit, head);
       if (w.n == 0) continue;
       if (!soft_wait(&q_free, (n_act++ & 1) ^ 1, a.ctrl, lane)) {
         ok = false;
@@ -813,18 +874,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
 
   if (warp == kFewWarps) {
     // ------------------------------ TMA loads ------------------------------
-    if (lane == 0) {
-      int kv = 0;
-      bool ok = true;
-      for (int it = 0; ok && unit_index(it) < n_units; ++it) {
-        const int e = unit_index(it) / a.Hkv, head = unit_index(it) - e * a.Hkv;
-        const AttnUnit u = a.units[e];
-        for (int kt = u.kt0; kt < u.kt1; ++kt, ++kv) {
-          const int s = kv % NS;
-          if (!wait_or_flag(&empty[s], ((kv / NS) & 1) ^ 1, a.ctrl)) {
-            ok = false;
-            break;
-          }
+    int kv = 0;
+    bool ok = true;
+    for (int it = 0; ok && unit_index(it) < n_units; ++it) {
+      const int unit = unit_index(it);
+      const int e = unit / a.Hkv, head = unit - e * a.Hkv;
+      const AttnUnit u = a.units[e];
+      for (int kt = u.kt0; kt < u.kt1; ++kt, ++kv) {
+        const int s = kv % NS;
+        if (!soft_wait(&empty[s], ((kv / NS) & 1) ^ 1, a.ctrl, lane)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
           mbar_expect_tx(&full[s], 2 * L::kTile);
           for (int z = 0; z < 2; ++z)
             for (int c = 0; c < D / 64; ++c)
@@ -832,8 +894,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
                      &full[s]);
         }
       }
-      drain_ring(full, NS, kv, a.ctrl);
     }
+    if (lane == 0) drain_ring(full, NS, kv, a.ctrl);
     return;
   }
 
@@ -842,7 +904,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   int kv = 0;
   bool ok = true;  // after a wait that ran out the warp only keeps its place in the barriers
   for (int it = 0; unit_index(it) < n_units; ++it) {
-    const int e = unit_index(it) / a.Hkv, head = unit_index(it) - e * a.Hkv;
+    const int unit = unit_index(it);
+    const int e = unit / a.Hkv, head = unit - e * a.Hkv;
     const AttnUnit u = a.units[e];
     const int rows = u.npos * a.G;
     // row i of the unit is (position i / G, head i % G of the group)
