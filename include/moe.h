@@ -421,9 +421,9 @@ typedef struct {
  * A query that sees no key (len < n) gets zeros.  Rows of out that belong to no sequence are
  * left as they were.  A sequence whose query rows are out of order or outside [0, T], or whose
  * keys lie outside [0, kv_rows) or number more than max_kv, is left out, its rows of out
- * untouched, and MOE_DEVERR_BAD_RANGE is set.  Sequences may share keys.  A key's value of
- * infinity or NaN reaches the queries that see it, and may reach queries before it within 128
- * keys of it.  Deterministic: the same call gives the same bits.
+ * untouched, and MOE_DEVERR_BAD_RANGE is set.  Sequences may share keys.  An infinity or NaN in
+ * a key or its value reaches the queries that see the key and no others (an infinite value as
+ * an infinity or NaN).  Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_attn_workspace_size(const moe_attn_shape* shape, int32_t n_seqs, int32_t T, int32_t max_kv,
                                            size_t* bytes);

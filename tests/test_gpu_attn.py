@@ -159,6 +159,50 @@ def test_infinities_in_keys_beyond_sight_and_unused_rows():
     assert torch.equal(out[:59], base[:59]) and torch.isnan(out[59].float()).all() and torch.equal(out[60], base[60])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,n,kv,bad", [
+    (4, 2, 128, 300, 300, [37, 150, 299]),
+    (4, 4, 64, 400, 400, [0, 127, 128, 255, 256, 399]),  # units of 256 positions
+    (16, 2, 128, 45, 45, [3, 31, 32]),                   # units of 32
+    (4, 2, 128, 33, 9000, [20, 8967, 8968, 8998, 8999]),  # cut into pieces
+    (6, 2, 64, 20, 9, [0, 8]),                           # rows that see no key at all
+    (4, 2, 128, 8, 8, [0, 5, 7]),                        # few rows
+    (4, 2, 64, 8, 135, [126, 127, 128, 134]),            # ... from one tile into the next
+    (8, 1, 128, 2, 9500, [9498, 9499]),                  # ... in pieces
+])
+def test_nonfinite_values_reach_only_the_queries_that_see_them(Hq, Hkv, d, n, kv, bad):
+    """Every other element keeps its bits; those columns of the rows that see the key are not finite."""
+    c = make(Hq, Hkv, d, [n], [kv], seed=34)
+    base, ws = run(c)
+    check(c, base)
+    first, gone = int(c["begin"][0]), torch.zeros(n, Hq, d, dtype=torch.bool, device=DEV)
+    for i, key in enumerate(bad):
+        head, col = i % Hkv, (i * 29 + 5) % d
+        c["v"][first + key, head, col] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+        gone[max(0, key - (kv - n)):, head * (Hq // Hkv):(head + 1) * (Hq // Hkv), col] = True
+    out, _ = run(c, ws)
+    assert abi.moe_ws_check(ws) == 0
+    assert torch.equal(~torch.isfinite(out.float()), gone)
+    assert torch.equal(out[~gone], base[~gone])
+
+
+def test_nonfinite_values_over_many_units():
+    """Calls of many units, every one with such values, back to back on one workspace."""
+    lens = [1 + (37 * i) % 150 for i in range(120)]
+    c = make(8, 2, 128, lens, [x + (i % 3) * 70 for i, x in enumerate(lens)], seed=35)
+    base, ws = run(c)
+    check(c, base, seqs=range(0, 120, 17))
+    off, begin, length = c["off"].tolist(), c["begin"].tolist(), c["len"].tolist()
+    gone = torch.zeros(c["T"], 8, 128, dtype=torch.bool, device=DEV)
+    for s in range(1, 120, 2):  # every other sequence: the units between stay clean
+        c["v"][begin[s] + length[s] - 1, 1, s % 128] = float("nan")
+        gone[off[s + 1] - 1, 4:, s % 128] = True
+    for _ in range(3):
+        out, _ = run(c, ws)
+        assert abi.moe_ws_check(ws) == 0
+        assert torch.equal(~torch.isfinite(out.float()), gone)
+        assert torch.equal(out[~gone], base[~gone])
+
+
 def test_bad_ranges_are_left_out():
     c = make(4, 2, 128, [30, 10, 5, 6, 7, 8], [40, 10, 5, 6, 7, 8], seed=24)
     c["begin"][1] = -1
