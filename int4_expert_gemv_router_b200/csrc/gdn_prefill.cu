@@ -1017,6 +1017,12 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
       if (vr + 8 * e < a.dv) *reinterpret_cast<float2*>(a.S_out + s_at + 8 * e * DK + t * 8) = S[t][e];
 }
 
+// The units of two slices come one an SM and round; where those of the last, partial round fill at most
+// half of the SMs they are cut into units of one slice, which are done sooner.
+__device__ __forceinline__ bool last_round_split(const GdnPrefillArgs& a, int unit, int units) {
+  const int full = units / a.n_sm * a.n_sm;
+  return unit >= full && 2 * (units - full) <= a.n_sm;
+}
 // NS = 0: one slice a warp and 64 rows a CTA, or two slices and 128 rows, as the plan says; the grid
 // is the former's, so that every other CTA of the latter leaves.
 template <int DK, int NS>
@@ -1057,7 +1063,7 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPre
   if (seq.n < 0) return;
   if constexpr (NS > 0) {
     gdn_scan<DK, NS>(a, a.slabs, seq, s, h, rb, smem, full);
-  } else if (chain) {
+  } else if (chain || last_round_split(a, (place * a.Hv + h) * ((blocks + 1) / 2) + rb / 2, a.n_seqs * a.Hv * ((blocks + 1) / 2))) {
     gdn_scan<DK, 1>(a, a.slabs, seq, s, h, rb, smem, full);
   } else if (rb % 2 == 0) {
     gdn_scan<DK, 2>(a, 2 * a.slabs, seq, s, h, rb / 2, smem, full);
