@@ -82,6 +82,7 @@ struct AttnArgs {
   int fill;          // pieces that keys are cut for; 0: nothing is cut
   int sort;          // units in order, longest first
   int few;           // the few-rows kernel's call
+  int self_plan;     // no plan kernel: every CTA finds its one unit for itself
   float scale_log2;  // scale * log2(e)
   const int32_t *offsets, *kv_begin, *kv_len;
   const uint16_t* v;
@@ -221,6 +222,56 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
     a.hdr->n_recs = s_recs;
     a.hdr->ticket = 0;
   }
+}
+
+// Calls of up to 32 sequences whose keys are not cut and whose units (a bound of them) are no more than
+// the SMs need no plan kernel: each CTA finds its one unit for itself (37 tokens: 13.7 -> 11.7 us).  (Cut
+// keys need the joins' counters cleared beforehand; one warp in the place of the plan's CTA there was no
+// faster: one token over 60,001 keys 25.0 -> 25.3, 32 tokens 38.9 -> 39.3.)
+constexpr int kWarpSeqs = 32;
+struct AttnWarpPlan {
+  AttnSeq seq;        // this lane's sequence (n < 0: left out, or none)
+  bool bad;
+  int blocks, first;  // its blocks, and those of the sequences before
+};
+__device__ __forceinline__ AttnWarpPlan attn_warp_plan(const AttnArgs& a, int lane) {
+  const bool in = lane < a.n_seqs;
+  const int r0 = in ? a.offsets[lane] : 0, r1 = in ? a.offsets[lane + 1] : 0;
+  const int kv0 = !in ? 0 : a.kv_begin ? a.kv_begin[lane] : r0, len = !in ? 0 : a.kv_begin ? a.kv_len[lane] : r1 - r0;
+  int seen = __shfl_up_sync(0xffffffffu, r0, 1);  // the largest offset before, 0 at least
+  seen = lane ? max(seen, 0) : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, seen, o);
+    if (lane >= o) seen = max(seen, v);
+  }
+  const bool ok = in && rows_ok(r0, r1, seen, a.T) && kv0 >= 0 && len >= 0 && len <= a.max_kv && kv0 <= a.kv_rows &&
+                  len <= a.kv_rows - kv0;
+  AttnWarpPlan p;
+  p.seq = AttnSeq{r0, ok ? r1 - r0 : -1, kv0, len};
+  p.bad = in && !ok;
+  p.blocks = ok ? (r1 - r0 + a.BP - 1) / a.BP : 0;
+  int sum = p.blocks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  p.first = sum - p.blocks;
+  return p;
+}
+// Without a plan kernel: block e of a call whose blocks are not cut, found by a warp (a CTA takes one
+// unit).  Returns the call's blocks.
+__device__ __forceinline__ int attn_self_plan(const AttnArgs& a, int e, int lane, AttnUnit& u) {
+  const AttnWarpPlan p = attn_warp_plan(a, lane);
+  if (blockIdx.x == 0 && p.bad) atomicOr(&a.ctrl->err, kErrBadRange);
+  const unsigned has = __ballot_sync(0xffffffffu, e >= p.first && e < p.first + p.blocks);
+  const int src = has ? __ffs(has) - 1 : 0;
+  const auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+  const AttnSeq q{from(p.seq.row0), from(p.seq.n), from(p.seq.kv0), from(p.seq.len)};
+  const int b = e - from(p.first), np = min(a.BP, q.n - b * a.BP), seen = q.len - q.n + b * a.BP + 1;
+  u = AttnUnit{q.row0 + b * a.BP, np, q.kv0, q.len, seen, 0, tiles_of(seen, np), -1, 0, 1};
+  return __shfl_sync(0xffffffffu, p.first + p.blocks, 31);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -376,7 +427,7 @@ __device__ __forceinline__ bool queue_draw(UnitQueue& q, const AttnArgs& a, int 
   }
   int u = 0;
   if (lane == 0) {
-    u = it ? (int)gridDim.x + atomicAdd(&a.hdr->ticket, 1) : (int)blockIdx.x;
+    u = !it ? (int)blockIdx.x : a.self_plan ? n_units : (int)gridDim.x + atomicAdd(&a.hdr->ticket, 1);
     if (u >= n_units) u = -1;
     q.unit[it & 1] = u;
     mbar_arrive(&q.full[it & 1]);
@@ -401,11 +452,11 @@ struct AttnWork {
   AttnUnit u;
   int np[2], nk[2], n;  // positions, key tiles of the piece; the larger of nk
 };
-__device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, int idx, int& head) {
+__device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, int idx, const AttnUnit& self, int& head) {
   AttnWork w;
   const int e = idx / a.Hkv;
   head = idx - e * a.Hkv;
-  w.u = a.units[e];
+  w.u = a.self_plan ? self : a.units[e];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     w.np[x] = max(0, min(a.PT, w.u.npos - x * a.PT));
@@ -487,6 +538,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_free, s_full[2][2], p_full[2][2],
       o_prev[2], o_done[2], o_free[2], v_raw[NS], drain[2];
   __shared__ UnitQueue queue;
+  __shared__ AttnUnit s_unit;
+  __shared__ int s_blocks;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_bad[4];  // unit it & 3: elements of its values were taken out (units go at most two ahead of a reader)
@@ -528,7 +581,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = s_tmem;  // columns: S of A 0.., S of B 128.., O of A 256.., O of B 384..
   pdl_wait();                    // the units are the plan kernel's, every input earlier work's
-  const int n_units = a.hdr->n_units;
+  if (a.self_plan) {
+    if (warp == 0) {
+      AttnUnit u;
+      const int blocks = attn_self_plan(a, (int)blockIdx.x / a.Hkv, lane, u);
+      if (lane == 0) {
+        s_unit = u;
+        s_blocks = blocks;
+      }
+    }
+    __syncthreads();
+  }
+  const int n_units = a.self_plan ? s_blocks * a.Hkv : a.hdr->n_units;
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -549,7 +613,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         break;
       }
       if (unit < 0) break;
-      const AttnWork w = attn_work(a, unit, head);
+      const AttnWork w = attn_work(a, unit, s_unit, head);
       const int np = x ? w.np[1] : w.np[0], nk = x ? w.nk[1] : w.nk[0];
       if (np == 0) continue;
       const int seen_r = pos < np ? w.u.seen + x * a.PT + pos : 0;  // keys this row sees (a row in use or 0)
@@ -743,7 +807,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         break;
       }
       if (unit < 0) break;
-      const AttnWork w = attn_work(a, unit, head);
+      const AttnWork w = attn_work(a, unit, s_unit, head);
       if (w.n == 0) continue;
       const int nk = x ? w.nk[1] : w.nk[0];
       if (!wait(&kv_full[kv % NS], (kv / NS) & 1)) break;
@@ -801,7 +865,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         break;
       }
       if (unit < 0) break;
-      const AttnWork w = attn_work(a, unit, head);
+      const AttnWork w = attn_work(a, unit, s_unit, head);
       if (w.n == 0) continue;
       if (!soft_wait(&q_free, (n_act++ & 1) ^ 1, a.ctrl, lane)) {
         ok = false;
@@ -865,7 +929,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
         break;
       }
       if (unit < 0) break;
-      const AttnWork w = attn_work(a, unit, head);
+      const AttnWork w = attn_work(a, unit, s_unit, head);
       if (lane == 0) s_bad[it & 3] = 0;
       __syncwarp();
       for (int j = max(0, max(w.u.seen, 0) / kAttnTile - w.u.kt0); j < w.n; ++j) {
@@ -933,13 +997,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 }
 __device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory"); }
 
-template <int D>
+// SELF: without a plan kernel (a template: the branches cost the cut calls' kernel registers, 0.4 us of 25 and 39)
+template <int D, bool SELF>
 __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_constant__ AttnArgs a, const uint16_t* q) {
   using L = FewSmem<D>;
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[NS], empty[NS];
   __shared__ int s_last;
+  __shared__ AttnUnit s_unit;
+  __shared__ int s_blocks;
   __shared__ float2 s_ml2[2][kFewWarps][kFewRows];  // by turns: a warp may still read one unit's while another is at the next's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
@@ -955,7 +1022,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   }
   __syncthreads();
   pdl_wait();
-  const int n_units = a.hdr->n_units;
+  if constexpr (SELF) {
+    if (warp == kFewWarps) {
+      AttnUnit u;
+      const int blocks = attn_self_plan(a, (int)blockIdx.x / a.Hkv, lane, u);
+      if (lane == 0) {
+        s_unit = u;
+        s_blocks = blocks;
+      }
+    }
+    __syncthreads();
+  }
+  const int n_units = SELF ? s_blocks * a.Hkv : a.hdr->n_units;
 
   if (warp == kFewWarps) {
     // ------------------------------ TMA loads ------------------------------
@@ -964,7 +1042,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
     for (int it = 0; ok && unit_index(it) < n_units; ++it) {
       const int unit = unit_index(it);
       const int e = unit / a.Hkv, head = unit - e * a.Hkv;
-      const AttnUnit u = a.units[e];
+      const AttnUnit u = SELF ? s_unit : a.units[e];
       for (int kt = u.kt0; kt < u.kt1; ++kt, ++kv) {
         const int s = kv % NS;
         if (!soft_wait(&empty[s], ((kv / NS) & 1) ^ 1, a.ctrl, lane)) {
@@ -991,7 +1069,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   for (int it = 0; unit_index(it) < n_units; ++it) {
     const int unit = unit_index(it);
     const int e = unit / a.Hkv, head = unit - e * a.Hkv;
-    const AttnUnit u = a.units[e];
+    const AttnUnit u = SELF ? s_unit : a.units[e];
     const int rows = u.npos * a.G;
     // row i of the unit is (position i / G, head i % G of the group)
     uint32_t qa[D / 16][4];
@@ -1171,7 +1249,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         v[c + 2] = x.z + y.z;
         v[c + 3] = x.w + y.w;
       }
-      if (u.slot >= 0) {
+      if (!SELF && u.slot >= 0) {
         const size_t prow = ((size_t)u.slot * a.Hkv + head) * a.rows_slot + row;
 #pragma unroll
         for (int c = 0; c < kPer; c += 4)
@@ -1188,7 +1266,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
       }
     }
-    if (u.slot < 0) continue;
+    if (SELF || u.slot < 0) continue;
     // ---- join the pieces: the CTA that finishes the last of a group joins the group in the place of
     // its first, the one that finishes the last group joins the groups.  Up to 16 pieces are one
     // group; more make groups of eight (one CTA alone would read a long cache's 70 pieces in 9 us,
@@ -1322,12 +1400,14 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
   // thousand: 38.5 against 36.3)
   a.sort = units > n_sm && !(few && blocks * a.Hkv <= 2 * n_sm);
   a.few = few;
-  cudaError_t e = launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
+  a.self_plan = a.n_seqs <= kWarpSeqs && !cut && units <= n_sm;
+  cudaError_t e = a.self_plan ? cudaSuccess : launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)std::min<long long>(n_sm, units));
   if (few) {
-    e = cudaFuncSetAttribute(k_attn_few<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
-    if (e == cudaSuccess) e = launch_pdl(k_attn_few<D>, grid, dim3(kFewThreads), FewSmem<D>::kBytes, s, a, q);
+    const auto fn = a.self_plan ? k_attn_few<D, true> : k_attn_few<D, false>;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
+    if (e == cudaSuccess) e = launch_pdl(fn, grid, dim3(kFewThreads), FewSmem<D>::kBytes, s, a, q);
   } else {
     e = cudaFuncSetAttribute(k_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes);
     if (e == cudaSuccess) e = launch_pdl(k_attn<D>, grid, dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
