@@ -69,7 +69,8 @@ struct AttnHdr {
 };
 
 constexpr int kAttnTile = 128;     // rows of a query tile and of a key tile
-constexpr int kAttnFill = 148;     // pieces aimed at (tile kernel): one per SM
+constexpr int kAttnRound = 148;    // a unit for every SM
+constexpr int kAttnFill = 222;     // pieces that keys are cut for (tile kernel; pieces after histories: 148 71.2 us, 222 66.8, 296 68.9)
 constexpr int kAttnFillFew = 296;  // and for few rows
 constexpr int kAttnMinPiece = 4;   // key tiles of a piece at least
 constexpr int kAttnMaxSlots = 2 * kAttnFillFew;
@@ -93,7 +94,7 @@ struct AttnArgs {
   AttnUnit* units;
   AttnRec* recs;
   int* done;         // [2][slot * Hkv + head], few rows: pieces finished of a group, groups of a block
-  float* part_o;     // [slot * Hkv + head][rows_slot][d]
+  float* part_o;     // [slot * Hkv + head], then k_attn: [d / 4][rows_slot][4], k_attn_few: [rows_slot][d]
   float2* part_ml;   // [slot * Hkv + head][rows_slot]: maximum (log2 units) and sum
   alignas(64) CUtensorMap map_q;
   alignas(64) CUtensorMap map_k;
@@ -138,9 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
   }
   __syncthreads();
   // Pieces of at most P tiles: with P >= the call's key tiles (over blocks and key heads) / fill the
-  // pieces of cut blocks number at most 2 fill <= kAttnMaxSlots (a block of t > P tiles makes
+  // pieces of cut blocks number at most 2 fill <= kAttnMaxSlots (a block of t > longest >= P tiles makes
   // ceil(t / P) < 2 t / P).
-  int P = 1 << 24;
+  int P = 1 << 24, longest = 1 << 24;  // a block of up to `longest` key tiles stays whole
   if (a.fill) {
     unsigned long long work = 0;
     int blocks = 0;
@@ -162,15 +163,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
       atomicAdd(&s_blocks, blocks);
     }
     __syncthreads();
-    // Few blocks (U of them over the key heads): at most W / P + U <= kAttnFill pieces, one round of
+    // Few blocks (U of them over the key heads): at most W / P + U <= kAttnRound pieces, one round of
     // the SMs (one token over 60,001 keys 37 -> 29 us, against 296).
-    const float U = (float)s_blocks * (float)a.Hkv, fill = 2.f * U <= kAttnFill ? kAttnFill - U : a.fill;
-    const float per = (float)s_work * (float)a.Hkv / fill;
-    // rounded up, and never below the quotient
-    P = per < 1e7f ? max(kAttnMinPiece, (int)(per * 1.0001f + 0.9999f)) : 1 << 24;
+    const float U = (float)s_blocks * (float)a.Hkv, work_all = (float)s_work * (float)a.Hkv;
+    const bool round = 2.f * U <= kAttnRound;
+    const auto tiles = [](float per) {  // rounded up, and never below the quotient
+      return per < 1e7f ? max(kAttnMinPiece, (int)(per * 1.0001f + 0.9999f)) : 1 << 24;
+    };
+    P = tiles(work_all / (round ? kAttnRound - U : a.fill));
+    // A block of no more key tiles than an SM's share is not in the way of the others: cut all the same,
+    // its partial results only cost (ragged prompts 101.6 us, whole 90.2).
+    longest = round || a.few ? P : tiles(work_all / kAttnRound);
   }
   // Place the units; longest first (a counting sort, two rounds) where a CTA has several.
-  const float to_bin = (float)(kPlanThreads - 1) / (float)(a.fill ? P : max(1, (a.max_kv + kAttnTile - 1) / kAttnTile));
+  const float to_bin = (float)(kPlanThreads - 1) / (float)(a.fill ? longest : max(1, (a.max_kv + kAttnTile - 1) / kAttnTile));
   for (int pass = a.sort ? 0 : 1; pass < 2; ++pass) {
     for (int s = warp; s < a.n_seqs; s += kPlanThreads / 32) {
       const AttnSeq q = seqs[s];
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
         const bool in = b * BP < q.n;
         const int np = min(BP, q.n - b * BP), seen = q.len - q.n + b * BP + 1, t = in ? tiles_of(seen, np) : 0;
         int len = t, pieces = in ? 1 : 0;
-        if (t > P) {  // equal pieces
+        if (t > longest) {  // equal pieces
           pieces = (t + P - 1) / P;
           len = (t + pieces - 1) / pieces;
           pieces = (t + len - 1) / len;
@@ -734,10 +740,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
           add_nonfinite(o, attn_value(a, w.u.kv0 + k0, head) + c * 32, (size_t)a.Hkv * D, k0, min(seen_r, w.u.kt1 * kAttnTile));
         }
         if (mine && w.u.slot >= 0) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c * 32);
+          // a row's four columns next to the next row's: whole lines a store
+          float4* dst = reinterpret_cast<float4*>(a.part_o) +
+                        (((size_t)w.u.slot * a.Hkv + head) * (D / 4) + c * 8) * a.rows_slot + brow;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+            dst[(size_t)i * a.rows_slot] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
                                  __uint_as_float(o[4 * i + 3]));
         } else if (mine) {
           uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
@@ -1332,49 +1340,61 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   }
 }
 
-// Joins the pieces of the cut blocks of k_attn (k_attn_few joins its own): a warp per row, a lane has
-// D / 32 columns; a row's pieces are added in a fixed order.
+// Joins the pieces of the cut blocks of k_attn (k_attn_few joins its own): a thread has eight columns of
+// a row, a CTA those of 128 rows; a row's pieces are added in order, four loaded at a time.
+constexpr int kJoinRows = 128, kJoinCols = 8;
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a) {
-  constexpr int EPL = D / 32, ROWS = 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kJoinRows) k_attn_join(const __grid_constant__ AttnArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int n_recs = a.hdr->n_recs, groups = (a.rows_slot * a.Hkv + ROWS - 1) / ROWS;  // of a block's rows
-  for (int item = blockIdx.x; item < n_recs * groups; item += gridDim.x) {
-    const AttnRec rec = a.recs[item / groups];
-    const int rows = rec.npos * a.G, i = item % groups * ROWS + warp;
-    if (i >= rows * a.Hkv) continue;
-    const int head = i / rows, row = i - head * rows, pos = row / a.G, sub = row - pos * a.G;
-    const size_t at0 = ((size_t)rec.slot * a.Hkv + head) * a.rows_slot + row, next = (size_t)a.Hkv * a.rows_slot;
-    // the maximum first: a lane a piece
-    float top = -INFINITY;
-    for (int p = lane; p < rec.pieces; p += 32) {
-      const float2 ml = a.part_ml[at0 + p * next];
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
+  const int n_recs = a.hdr->n_recs, row_parts = (a.rows_slot + kJoinRows - 1) / kJoinRows;
+  const int per = row_parts * (D / kJoinCols) * a.Hkv;  // of a block
+  for (int item = blockIdx.x; item < n_recs * per; item += gridDim.x) {
+    const AttnRec rec = a.recs[item / per];
+    const int rest = item % per, head = rest % a.Hkv, part = rest / a.Hkv;
+    const int c4 = part % (D / kJoinCols) * 2, row = part / (D / kJoinCols) * kJoinRows + threadIdx.x;
+    if (row >= rec.npos * a.G) continue;
+    const size_t base = (size_t)rec.slot * a.Hkv + head;
+    const float2* pml = a.part_ml + base * a.rows_slot + row;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) + (base * (D / 4) + c4) * a.rows_slot + row;
+    const size_t ml_step = (size_t)a.Hkv * a.rows_slot, o_step = ml_step * (D / 4);
+    float m = -INFINITY, sum = 0.f, o[kJoinCols] = {};
+    for (int p = 0; p < rec.pieces; p += 4) {
+      float2 ml[4];
+      float4 v[4][2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float b = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o[EPL] = {};
-#pragma unroll 4
-    for (int p = 0; p < rec.pieces; ++p) {
-      const size_t at = at0 + p * next;
-      const float2 ml = a.part_ml[at];
-      float v[EPL];
-      if constexpr (EPL == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at * D + lane * EPL);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * EPL);
-      // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
-      const float f = ml.y == 0.f ? 0.f : ex2(ml.x - b);
-      sum = fmaf(ml.y, f, sum);
+      for (int x = 0; x < 4; ++x) {
+        const int q = min(p + x, rec.pieces - 1);
+        ml[x] = __ldcg(pml + q * ml_step);
+        v[x][0] = __ldcg(po + q * o_step);
+        v[x][1] = __ldcg(po + q * o_step + a.rows_slot);
+      }
+      float mn = m;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = ml.y == 0.f ? o[e] : fmaf(v[e], f, o[e]);
+      for (int x = 0; x < 4; ++x)
+        if (ml[x].y != 0.f) mn = fmaxf(mn, ml[x].x);
+      const float base_m = mn == -INFINITY ? 0.f : mn, back = ex2(m - base_m);
+      m = mn;
+      sum *= back;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) o[e] *= back;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        // a sum of 0: the row sees none of the piece's keys, and what it holds does not count
+        if (p + x >= rec.pieces || ml[x].y == 0.f) continue;
+        const float f = ex2(ml[x].x - base_m);
+        sum = fmaf(ml[x].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) o[e] = fmaf(reinterpret_cast<const float*>(v[x])[e], f, o[e]);
+      }
     }
+    const int pos = row / a.G, sub = row - pos * a.G;
     const float inv = 1.0f / sum;
-    uint16_t* dst = a.out + ((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + lane * EPL;
+    uint32_t r[kJoinCols / 2];
 #pragma unroll
-    for (int e = 0; e < EPL; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = rec.seen + pos > 0 ? pack_bf16(o[e] * inv, o[e + 1] * inv) : 0u;
+    for (int e = 0; e < kJoinCols; e += 2) r[e / 2] = rec.seen + pos > 0 ? pack_bf16(o[e] * inv, o[e + 1] * inv) : 0u;
+    *reinterpret_cast<uint4*>(a.out + ((size_t)(rec.row + pos) * a.Hq + (size_t)head * a.G + sub) * D + c4 * 4) =
+        make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -1413,8 +1433,9 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
     if (e == cudaSuccess) e = launch_pdl(k_attn<D>, grid, dim3(kAttnThreads), AttnSmem<D>::kBytes, s, a);
   }
   if (e != cudaSuccess || few || !cut) return e;
-  const long long rows = std::min<long long>(blocks, kAttnMaxSlots / 2) * a.rows_slot * a.Hkv;
-  return launch_pdl(k_attn_join<D>, dim3((unsigned)std::min<long long>((rows + 3) / 4, 8 * n_sm)), dim3(128), 0, s, a);
+  const long long parts = std::min<long long>(blocks, kAttnMaxSlots / 2) * a.Hkv * (D / kJoinCols) *
+                          ((a.rows_slot + kJoinRows - 1) / kJoinRows);
+  return launch_pdl(k_attn_join<D>, dim3((unsigned)std::min<long long>(parts, 8 * n_sm)), dim3(kJoinRows), 0, s, a);
 }
 
 cudaError_t launch_attn(AttnArgs& a, bool few, const void* q, const void* k, const void* v, cudaStream_t s) {
