@@ -222,6 +222,33 @@ def test_bad_ranges_are_left_out():
     assert (out[40:] == 7.0).all()
 
 
+@pytest.mark.parametrize("lens,kv", [
+    ([1, 2, 1, 1, 3], [300, 20, 70, 9, 3]),               # few rows
+    ([1, 2, 1, 1, 3], [3000, 20, 70, 9, 3]),              # ... with keys in pieces
+    ([90, 20, 1, 33, 3], [300, 20, 70, 33, 3]),           # tiles
+    ([90, 20, 1, 33, 3], [9000, 20, 70, 33, 3]),          # ... with keys in pieces
+    ([90, 20, 1, 33, 3] * 8, [300, 20, 70, 33, 3] * 8),   # more sequences than a warp has lanes
+    ([1, 2, 1, 1, 3] * 8, [900, 20, 70, 9, 3] * 8),
+])
+def test_bad_ranges_on_every_path(lens, kv):
+    """Keys out of range, then query rows out of order: the sequences concerned, and no others."""
+    c = make(8, 2, 128, lens, kv, seed=36)
+    ws = workspace(c)
+    off = c["off"].tolist()
+    begin = c["begin"].clone()
+    begin[1], begin[3] = -1, c["rows"] - 2
+    out, _ = run(dict(c, begin=begin), ws)
+    assert abi.moe_ws_check(ws) == abi.DEVERR_BAD_RANGE and abi.moe_ws_check(ws) == 0
+    check(c, out, seqs=[s for s in range(len(lens)) if s not in (1, 3)])
+    assert all((out[off[s]:off[s + 1]] == 7.0).all() for s in (1, 3))
+    offsets = c["off"].clone()
+    offsets[2] = offsets[1] - 1  # sequence 1 would end before it begins; sequence 2 begin in sequence 0's rows
+    out, _ = run(dict(c, off=offsets), ws)
+    assert abi.moe_ws_check(ws) == abi.DEVERR_BAD_RANGE
+    check(c, out, seqs=[s for s in range(len(lens)) if s not in (1, 2)])
+    assert all((out[off[s]:off[s + 1]] == 7.0).all() for s in (1, 2))
+
+
 def test_rows_outside_sequences_and_shared_keys():
     c = make(4, 2, 128, [20, 33], [64, 64], seed=26, pad=6)
     c["begin"][1] = c["begin"][0]  # both read the same keys
