@@ -321,6 +321,45 @@ def test_captured_and_on_two_streams():
         assert torch.equal(o, ref[i % 2])
 
 
+@pytest.mark.parametrize("few", [False, True])
+def test_small_calls_captured_with_other_lengths(few):
+    """Two small calls without a plan kernel on one workspace in one graph, replayed over other lengths
+    (as many rows and room for keys) and over a sequence that went out of range."""
+    lens = [[1, 3, 0, 1, 1], [2, 0, 1, 1, 2]] if few else [[40, 3, 0, 70, 1], [5, 60, 44, 0, 5]]
+    kv = [[30, 9, 4, 200, 1], [2, 7, 1, 90, 400]] if few else [[40, 90, 4, 70, 300], [5, 60, 100, 7, 5]]
+    names = ("q", "k", "v", "off", "begin", "len")
+    cs = []
+    for i in range(2):
+        c = make(8, 2, 64, lens[i], kv[i], seed=37 + i)
+        rows = 700
+        for x in ("k", "v"):
+            c[x] = torch.cat([c[x], c[x].new_full((rows - c["rows"], 2, 64), float("nan"))])
+        cs.append(dict(c, rows=rows, max_kv=512))
+    assert cs[0]["T"] == cs[1]["T"]
+    for c in cs:
+        check(c, run(c)[0])
+    ref = [run(c)[0] for c in cs]
+    c = dict(cs[0], **{x: cs[0][x].clone() for x in names})
+    ws, s = workspace(c), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        first, _ = run(c, ws)
+        second, _ = run(c, ws)
+    for i in (0, 1, 0):
+        for x in names:
+            c[x].copy_(cs[i][x])
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, ref[i]) and torch.equal(second, ref[i]) and abi.moe_ws_check(ws) == 0
+    c["len"][0] = 513
+    gr.replay()
+    torch.cuda.synchronize()
+    assert abi.moe_ws_check(ws) == abi.DEVERR_BAD_RANGE
+    n = lens[0][0]
+    assert (first[:n] == 7.0).all() and torch.equal(first[n:], ref[0][n:])
+
+
 def test_hybrid_prompt_then_token():
     """A prompt through a Gated DeltaNet layer and an attention layer, one workspace for both, then
     one token of each sequence through the decode step and the attention over the grown cache."""
