@@ -1185,10 +1185,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
         pl[2 * n] = pack_bf16(p0 - bf_lo(p[2 * n]), p1 - bf_hi(p[2 * n]));
         pl[2 * n + 1] = pack_bf16(p2 - bf_lo(p[2 * n + 1]), p3 - bf_hi(p[2 * n + 1]));
       }
-      // keys that not every row sees: this warp cleans its own
+      // keys that not every row sees: this warp cleans its own.  With one position a unit no row sees
+      // the keys from u.seen on (the sequence's last ones, if the position is not), so they are all cleared.
       bool bad = false;
       if (key0 + 16 > u.seen) {
-        bad = __any_sync(0xffffffffu, clean_rows<D>(tv, warp * 16, warp * 16 + 16, u.len - kt * kAttnTile, u.npos > 1, lane));
+        const int end = u.npos > 1 ? u.len : max(u.seen, 0);
+        bad = __any_sync(0xffffffffu, clean_rows<D>(tv, warp * 16, warp * 16 + 16, end - kt * kAttnTile, u.npos > 1, lane));
         proxy_fence();  // before the next copy into the tile
         __syncwarp();
       }

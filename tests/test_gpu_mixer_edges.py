@@ -1,0 +1,47 @@
+"""GPU tests of what the token mixers (moe_attn_forward, moe_gdn_prefill) promise beside their
+sums: who an infinity or NaN reaches, the same bits from the same call, workspaces sized once.
+Inputs and oracle checks are those of the operators' own tests."""
+import pytest
+import torch
+
+from int4_expert_gemv_router_b200 import abi, build
+from test_gpu_attn import check, make, run
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,lens,kv,max_kv", [
+    (9, 1, [3, 0], [40, 5], 40),
+    (12, 1, [2, 1, 1, 1], [130, 3, 129, 1], 512),
+    (16, 1, [2, 0], [2, 0], 2),                   # a whole prompt of two tokens
+    (32, 2, [3, 0, 0], [128, 7, 0], 128),         # the last key of a tile, two key heads
+    (16, 1, [2, 0], [129, 9], 129),               # hidden keys are a tile of their own
+    (16, 1, [3, 0, 0], [9500, 3, 0], 9500),       # keys in pieces
+    (24, 2, [2, 1, 1, 1], [3000, 700, 3, 1], 3000),
+    (9, 1, [3, 1, 0, 1], [1, 1, 0, 1], 1),        # queries that see no key at all beside one that does
+])
+def test_nonfinite_values_with_one_position_a_unit(Hq, Hkv, d, lens, kv, max_kv):
+    """More than eight query heads a key head: units of one position, which do not see the last keys of
+    their sequence.  Every other element keeps its bits."""
+    c = dict(make(Hq, Hkv, d, lens, kv, seed=40 + Hq + d), max_kv=max_kv)
+    base, ws = run(c)
+    check(c, base)
+    off, begin = c["off"].tolist(), c["begin"].tolist()
+    gone = torch.zeros(c["T"], Hq, d, dtype=torch.bool, device=DEV)
+    for s, n in enumerate(lens):
+        for i in range(min(2, n, kv[s])):  # the last key (its query alone sees it) and the one before
+            key, head, col = kv[s] - 1 - i, i % Hkv, (s * 29 + i * 7 + 5) % d
+            c["v"][begin[s] + key, head, col] = (float("nan"), float("inf"), -float("inf"))[(s + i) % 3]
+            at = slice(off[s] + max(0, key - (kv[s] - n)), off[s + 1])
+            gone[at, head * (Hq // Hkv):(head + 1) * (Hq // Hkv), col] = True
+    out, _ = run(c, ws)
+    assert abi.moe_ws_check(ws) == 0
+    assert torch.equal(~torch.isfinite(out.float()), gone)
+    assert torch.equal(out[~gone], base[~gone])
