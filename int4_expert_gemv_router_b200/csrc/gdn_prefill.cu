@@ -151,12 +151,10 @@ __device__ __forceinline__ bool gdn_chain(const GdnPrefillArgs& a, int longest, 
 
 __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs a) {
   __shared__ int sh[32];
-  __shared__ int bins[kPlanThreads];
   __shared__ int s_longest;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
-  bins[tid] = 0;
   if (tid == 0) s_longest = 0;
   int seen = 0, chunks = 0;
   for (int base = 0; base < a.n_seqs; base += kPlanThreads) {
@@ -182,19 +180,38 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs 
     for (int c = lane; c * kGdnChunk < q.n; c += 32)
       a.chunks[q.chunk0 + c] = GdnChunk{q.row0 + c * kGdnChunk, min(kGdnChunk, q.n - c * kGdnChunk)};
   }
-  // sequences by length, longest first, in kPlanThreads classes
-  const int per = a.T / (kPlanThreads - 1) + 1;
+  // Sequences by length, longest first, in kPlanThreads classes; inside a class by number, so that the
+  // order (which may decide a sequence's slices, and with them its bits) is the call's and not the
+  // warps': a warp takes consecutive sequences, and its places in a class follow the earlier warps'.
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int s_bins[kWarps][kPlanThreads];
+  for (int w = 0; w < kWarps; ++w) s_bins[w][tid] = 0;
+  __syncthreads();
+  const int per = a.T / (kPlanThreads - 1) + 1, share = (a.n_seqs + kPlanThreads - 1) / kPlanThreads * 32;
+  const int end = min(a.n_seqs, (warp + 1) * share);
   for (int pass = 0; pass < 2; ++pass) {
-    for (int s = tid; s < a.n_seqs; s += kPlanThreads) {
-      const int bin = kPlanThreads - 1 - max(0, a.seqs[s].n) / per;
-      const int at = atomicAdd(&bins[bin], 1);
-      if (pass) a.order[at] = s;
+    for (int base = warp * share; base < end; base += 32) {
+      const int i = base + lane;
+      const int bin = i < end ? kPlanThreads - 1 - max(0, a.seqs[i].n) / per : kPlanThreads;
+      const unsigned same = __match_any_sync(0xffffffffu, bin);
+      const int at = i < end ? s_bins[warp][bin] + __popc(same & ((1u << lane) - 1)) : 0;
+      __syncwarp();  // every lane has read its class's count
+      if (i < end) {
+        if (pass) a.order[at] = i;
+        if (lane == __ffs(same) - 1) s_bins[warp][bin] += __popc(same);
+      }
+      __syncwarp();
     }
     __syncthreads();
     if (!pass) {
-      int total = 0;
-      const int first = block_excl_sum(bins[tid], total, sh);
-      bins[tid] = first;
+      int count = 0, total = 0;
+      for (int w = 0; w < kWarps; ++w) count += s_bins[w][tid];
+      int first = block_excl_sum(count, total, sh);
+      for (int w = 0; w < kWarps; ++w) {
+        const int n = s_bins[w][tid];
+        s_bins[w][tid] = first;
+        first += n;
+      }
       __syncthreads();
     }
   }

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from int4_expert_gemv_router_b200 import abi, build
+import test_gpu_gdn_prefill as gdn
 from test_gpu_attn import check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,29 @@ def test_nonfinite_values_with_one_position_a_unit(Hq, Hkv, d, lens, kv, max_kv)
     assert abi.moe_ws_check(ws) == 0
     assert torch.equal(~torch.isfinite(out.float()), gone)
     assert torch.equal(out[~gone], base[~gone])
+
+
+@pytest.mark.parametrize("n,H", [(48, 32), (300, 8)])
+def test_prompts_of_one_length_keep_their_bits(n, H):
+    """More sequences than a plan without its kernel takes, all of one length class, and a last round of
+    units that is cut: the same call gives the same bits, however busy the GPU is, and sequences of
+    the same inputs differ only where the cut falls, in the call's order."""
+    c = gdn.make(H // 2, H, 128, 128, [64] * n, seed=50)
+    for x in ("q", "k", "v", "g", "beta"):
+        c[x] = c[x][:64].repeat(n, *[1] * (c[x].dim() - 1))
+    c["S"][:] = c["S"][:1].clone()
+    out, S, ws = gdn.run(c)
+    gdn.check(c, out, S, seqs=(0, n - 1))
+    a, side = torch.randn(2048, 2048, device=DEV), torch.cuda.Stream()
+    for i in range(30):
+        if i % 2:
+            with torch.cuda.stream(side):
+                a = (a @ a).clamp(-1, 1)
+        again, S_again, _ = gdn.run(c, ws=ws)
+        assert torch.equal(out, again) and torch.equal(S, S_again)
+    torch.cuda.synchronize()
+    # heads of a state from one slice or two: all of the former come last
+    for h in range(H):
+        same = (S[:, h] == S[0, h]).flatten(1).all(1)
+        first = int(same.long().argmin()) if not same.all() else n
+        assert same[:first].all() and not same[first:].any()
