@@ -245,26 +245,14 @@ __device__ __forceinline__ AttnWarpPlan attn_warp_plan(const AttnArgs& a, int la
   const bool in = lane < a.n_seqs;
   const int r0 = in ? a.offsets[lane] : 0, r1 = in ? a.offsets[lane + 1] : 0;
   const int kv0 = !in ? 0 : a.kv_begin ? a.kv_begin[lane] : r0, len = !in ? 0 : a.kv_begin ? a.kv_len[lane] : r1 - r0;
-  int seen = __shfl_up_sync(0xffffffffu, r0, 1);  // the largest offset before, 0 at least
-  seen = lane ? max(seen, 0) : 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, seen, o);
-    if (lane >= o) seen = max(seen, v);
-  }
+  const int seen = warp_excl_max(r0, lane);
   const bool ok = in && rows_ok(r0, r1, seen, a.T) && kv0 >= 0 && len >= 0 && len <= a.max_kv && kv0 <= a.kv_rows &&
                   len <= a.kv_rows - kv0;
   AttnWarpPlan p;
   p.seq = AttnSeq{r0, ok ? r1 - r0 : -1, kv0, len};
   p.bad = in && !ok;
   p.blocks = ok ? (r1 - r0 + a.BP - 1) / a.BP : 0;
-  int sum = p.blocks;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
-  }
-  p.first = sum - p.blocks;
+  p.first = warp_incl_sum(p.blocks, lane) - p.blocks;
   return p;
 }
 // Without a plan kernel: block e of a call whose blocks are not cut, found by a warp (a CTA takes one

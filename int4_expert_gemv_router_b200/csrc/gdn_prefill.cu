@@ -121,22 +121,12 @@ struct GdnWarpPlan {
 __device__ __forceinline__ GdnWarpPlan gdn_warp_plan(const GdnPrefillArgs& a, int lane) {
   const bool in = lane < a.n_seqs;
   const int r0 = in ? a.offsets[lane] : 0, r1 = in ? a.offsets[lane + 1] : 0;
-  int seen = lane ? __shfl_up_sync(0xffffffffu, r0, 1) : (__shfl_up_sync(0xffffffffu, r0, 1), 0);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, seen, o);
-    if (lane >= o) seen = max(seen, v);
-  }
+  const int seen = warp_excl_max(r0, lane);
   GdnWarpPlan p;
-  const bool ok = in && rows_ok(r0, r1, max(seen, 0), a.T);
+  const bool ok = in && rows_ok(r0, r1, seen, a.T);
   p.bad = in && !ok;
   p.nc = ok ? (r1 - r0 + kGdnChunk - 1) / kGdnChunk : 0;
-  int sum = p.nc;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
-  }
+  const int sum = warp_incl_sum(p.nc, lane);
   p.n_chunks = __shfl_sync(0xffffffffu, sum, 31);
   p.seq = GdnSeq{r0, ok ? r1 - r0 : -1, sum - p.nc};
   return p;

@@ -65,6 +65,27 @@ __device__ __forceinline__ int block_excl_sum(int v, int& carry, int* sh) {
   return r;
 }
 
+// The same over one warp, a lane a sequence: the largest v of the lanes before (0 at least), and the sum
+// of v up to and with this lane.
+__device__ __forceinline__ int warp_excl_max(int v, int lane) {
+  v = __shfl_up_sync(0xffffffffu, v, 1);  // every lane shuffles: no lane may read one that does not
+  v = lane ? max(v, 0) : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = max(v, u);
+  }
+  return v;
+}
+__device__ __forceinline__ int warp_incl_sum(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
 // Sequence i's rows [a, b) are usable when the offsets are in order up to here and inside
 // [0, T]: a at least every earlier offset (seen: their maximum, 0 at least), a <= b <= T.
 // The usable sequences of a call are then disjoint.

@@ -72,3 +72,24 @@ def test_prompts_of_one_length_keep_their_bits(n, H):
         same = (S[:, h] == S[0, h]).flatten(1).all(1)
         first = int(same.long().argmin()) if not same.all() else n
         assert same[:first].all() and not same[first:].any()
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33])
+def test_offsets_checked_around_a_warp_of_sequences(n):
+    """A call's offsets are checked a lane a sequence up to 32 of them: one range out of order, at the first,
+    a middle and the last place; the sequence is left out and no other."""
+    lens = [1 + i % 3 for i in range(n)]
+    c = gdn.make(1, 2, 64, 32, lens, seed=51, pad=2)
+    ws = gdn.workspace(c)
+    for at in sorted({0, n // 2, n - 1}):
+        off = c["off"].clone()
+        off[at + 1] = off[at] - 1  # this one ends before it begins, the next begins in an earlier one's rows
+        d = dict(c, off=off)
+        out, S, _ = gdn.run(d, ws=ws)
+        assert abi.moe_ws_check(ws) == abi.DEVERR_BAD_RANGE and abi.moe_ws_check(ws) == 0
+        left = [s for s in (at, at + 1) if s < n]
+        gdn.check(d, out, S, seqs=[s for s in range(n) if s not in left])
+        assert all((S[s] == 9.0).all() for s in left)
+    out, S, _ = gdn.run(c, ws=ws)
+    assert abi.moe_ws_check(ws) == 0
+    gdn.check(c, out, S)
