@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
   __shared__ int s_slots, s_recs, s_blocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, BP = a.BP;
   AttnSeq* seqs = a.n_seqs <= kPlanSeqs ? s_seqs : a.seqs;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   if (tid == 0) {
     s_work = 0;
     s_slots = s_recs = s_blocks = 0;
@@ -539,7 +539,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   __shared__ int s_abort;
   __shared__ int s_bad[4];  // unit it & 3: elements of its values were taken out (units go at most two ahead of a reader)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte tiles
   const uint32_t ring = smem + 2 * L::kTile;
 
@@ -576,6 +575,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = s_tmem;  // columns: S of A 0.., S of B 128.., O of A 256.., O of B 384..
   pdl_wait();                    // the units are the plan kernel's, every input earlier work's
+  pdl_launch_dependents();
   if (a.self_plan) {
     if (warp == 0) {
       AttnUnit u;
@@ -1029,7 +1029,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   __shared__ int s_blocks;
   __shared__ float2 s_ml2[2][kFewWarps][kFewRows];  // by turns: a warp may still read one unit's while another is at the next's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* sums = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + NS * 2 * L::kTile);
   if (warp == kFewWarps && lane < 2 && a.kv_rows > 0) prefetch_map(lane ? &a.map_v : &a.map_k);
@@ -1042,6 +1041,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
   }
   __syncthreads();
   pdl_wait();
+  pdl_launch_dependents();
   if constexpr (SELF) {
     if (warp == kFewWarps) {
       AttnUnit u;
@@ -1359,8 +1359,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
 constexpr int kJoinRows = 128, kJoinCols = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinRows) k_attn_join(const __grid_constant__ AttnArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int n_recs = a.hdr->n_recs, row_parts = (a.rows_slot + kJoinRows - 1) / kJoinRows;
   const int per = row_parts * (D / kJoinCols) * a.Hkv;  // of a block
   for (int item = blockIdx.x; item < n_recs * per; item += gridDim.x) {

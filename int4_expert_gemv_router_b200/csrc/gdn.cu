@@ -60,8 +60,6 @@ __global__ void __launch_bounds__(kGdnWarps * 32) k_gdn_step(const GdnArgs a) {
   const int kh = h / (a.Hv / a.Hk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* Sh = a.S + (size_t)bh * a.dv * DK;
-  // the next kernel on the stream may start launching (it waits for this one where it must)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the rows this warp owns, loaded first so that their latency overlaps the normalisation
   float row[kGdnRowsPerWarp][EPL];
@@ -92,6 +90,9 @@ __global__ void __launch_bounds__(kGdnWarps * 32) k_gdn_step(const GdnArgs a) {
   // from here on every read and write waits for it to have finished.  Without that launch
   // attribute the wait returns at once.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now may the next kernel on the stream start (it waits for this one where it must): every
+  // kernel before this one is done then, so a state that an earlier step writes is not read too soon
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // k and q of this head's key head: warp 0 normalises k, warp 1 q (fp32 sums of squares)
   if (warp < 2) {
     const uint16_t* src = (warp == 0 ? a.k : a.q) + ((size_t)b * a.Hk + kh) * DK;

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs 
   __shared__ int sh[32];
   __shared__ int s_longest;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   if (tid == 0) s_longest = 0;
   int seen = 0, chunks = 0;
   for (int base = 0; base < a.n_seqs; base += kPlanThreads) {
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
   __shared__ float s_pm[2];             // the largest G_i - G_j, j <= i (0 where nothing grows)
   __shared__ float s_red[2][6];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int chunk = blockIdx.x / a.Hk, kh = blockIdx.x - chunk * a.Hk;
   GdnChunk C;
   if (a.warp_plan) {
@@ -1037,13 +1037,13 @@ __global__ void __launch_bounds__(256) k_gdn_scan(const __grid_constant__ GdnPre
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[2];
   uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   pdl_wait();
+  pdl_launch_dependents();
   const int blocks = (a.dv + kGdnSlab * a.slabs - 1) / (kGdnSlab * a.slabs), per = a.Hv * blocks;
   const int place = blockIdx.x / per, rest = blockIdx.x % per, h = rest / blocks, rb = rest - h * blocks;
   int s;

@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   const int K = (MODE == kModeDown) ? a.I : a.H;
   const int nK = K / kKC;
   const int NR = a.n_rows;  // weight rows per unit (the MMA's N): 128 or 256
-  pdl_launch_dependents();
   const GemmSmem P = gemm_smem<BITS, MODE>();
   const uint32_t wbytes = MODE == kModeRouter ? (uint32_t)(kTok * kKC * 2) : (uint32_t)kWBytes;  // per stage
   // stage tiles start on 1024-byte boundaries (128-byte swizzle atoms)
@@ -265,6 +264,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   const uint32_t tmem = s_tmem;
   // the setup above overlaps the kernel before; the work units and every input are its output
   pdl_wait();
+  pdl_launch_dependents();
   const int n_units = *a.n_units;
   const int my_units = n_units > (int)blockIdx.x ? (n_units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
@@ -660,8 +660,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
 // ---------------------------------------------------------------------------------------
 __global__ void k_norms(const uint16_t* x, int T, int H, const uint16_t* wr, const uint16_t* wsg, int E,
                         double* xnorm, double* wnorm) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   const int rows = T + E + 1;
   if (warp >= rows) return;
@@ -721,8 +721,8 @@ __device__ __forceinline__ double warp_dot_exact(const uint16_t* a, const uint16
 constexpr int kRouteCand = 96;
 
 __global__ void __launch_bounds__(256) k_gate(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int wl = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * 8 + wl;
   if (t >= a.T) return;
@@ -731,8 +731,8 @@ __global__ void __launch_bounds__(256) k_gate(PrefillArgs a) {
 }
 
 __global__ void __launch_bounds__(256) k_route(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   __shared__ double s_cl[8][kRouteCand];  // candidates' fp32 logits (with bias): the order key
   __shared__ double s_cu[8][kRouteCand];  // and their certified upper bounds
   __shared__ int s_ce[8][kRouteCand];
@@ -883,8 +883,8 @@ __device__ __forceinline__ bool remote_expert(const PrefillArgs& a, int e) {
 }
 
 __global__ void __launch_bounds__(kGroupThreads) k_ghist(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   extern __shared__ int hsm[];  // [E]
   const int E = a.E, n = a.T * a.k;
   for (int e = threadIdx.x; e < E; e += kGroupThreads) hsm[e] = 0;
@@ -905,8 +905,8 @@ __global__ void __launch_bounds__(kGroupThreads) k_ghist(PrefillArgs a) {
 }
 
 __global__ void __launch_bounds__(1024) k_gcol(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int e = blockIdx.x * 32 + (threadIdx.x >> 5);
   if (e >= a.E) return;
@@ -978,8 +978,8 @@ __device__ void block_scan4(int E, F val, int* out, int* wsum) {
 }
 
 __global__ void __launch_bounds__(kGroupThreads) k_gplace(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   extern __shared__ int wc[];  // [8][E]: per-warp counts, then per-warp running slots
   __shared__ int s_off[kMaxExperts + 1];
   __shared__ int s_wsum[kGroupThreads / 32 + 1];
@@ -1063,8 +1063,8 @@ __global__ void __launch_bounds__(kGroupThreads) k_gplace(PrefillArgs a) {
 // xg[p] = x[order[p] / k] for every grouped pair position p < offsets[E]: the routed gate/up
 // GEMM then reads each expert's tokens as consecutive rows.  One warp per row.
 __global__ void __launch_bounds__(256) k_permute(PrefillArgs a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   // warps [0, T*k): xg row p (valid pairs only); with perm, warps [T*k, T*k + T): xp row t
   const int p = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   const int n_pairs = a.T * a.k;
@@ -1087,8 +1087,8 @@ __global__ void __launch_bounds__(256) k_permute(PrefillArgs a) {
 }
 
 __global__ void k_finalize(const float* acc, const uint16_t* residual, uint16_t* out, size_t n) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n) out[i] = f2bf(acc[i] + (residual ? bf1(residual[i]) : 0.f));
 }
@@ -1096,8 +1096,8 @@ __global__ void k_finalize(const float* acc, const uint16_t* residual, uint16_t*
 // store), grid-stride; for 16-byte aligned buffers.  acc is read for the last time: streaming
 // loads.
 __global__ void __launch_bounds__(256) k_finalize8(const float4* acc, const uint4* residual, uint4* out, size_t n8) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += (size_t)gridDim.x * blockDim.x) {
     const float4 a0 = __ldcs(acc + 2 * i), a1 = __ldcs(acc + 2 * i + 1);
     const uint4 r = residual ? __ldcs(residual + i) : make_uint4(0, 0, 0, 0);
@@ -1111,8 +1111,8 @@ __global__ void __launch_bounds__(256) k_finalize8(const float4* acc, const uint
 }
 
 __global__ void k_router_units(GemmUnit* units, int* n_units, int T, int E) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   // E rows in tiles of 128 x tokens in tiles of 128 (the shared-expert gate logit is
   // computed exactly by k_route)
   const int mt_n = (E + 127) / 128;

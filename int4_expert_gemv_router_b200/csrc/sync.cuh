@@ -82,9 +82,11 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* b) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Programmatic dependent launch: the kernel after this one on the stream may start launching
-// now (it waits for this one's completion where it must) ...
+// now (it waits for this one's completion where it must).  Called behind pdl_wait: what starts
+// then finds every kernel but this one done.  Called before it, this kernel could still be waiting
+// for an earlier one while the next kernel reads ahead of its own wait (MOE_GDN_EARLY_STATE).
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// ... and this kernel waits, before its first read of what earlier work wrote, until the kernel
+// This kernel waits, before its first read of what earlier work wrote, until the kernel
 // before it has finished and its writes are visible (at once when not launched as a dependent).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Per-thread L2 prefetch of the 128-byte line holding p (a hint: no register result, no

@@ -93,3 +93,62 @@ def test_offsets_checked_around_a_warp_of_sequences(n):
     out, S, _ = gdn.run(c, ws=ws)
     assert abi.moe_ws_check(ws) == 0
     gdn.check(c, out, S)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("between", ["attention", "prompt", "router", "step"])
+def test_early_state_reads_behind_a_kernel_that_writes_another(between, graph):
+    """MOE_GDN_EARLY_STATE asks that the kernel right before the step does not write its state.  The one
+    before that may: prompt (writes S), one other small call, early step on S, over and over, gives the
+    bits of the plain steps."""
+    Hk, H, d, n, rounds = 2, 4, 64, 2, 6
+    c = gdn.make(Hk, H, d, d, [300, 40], seed=52)
+    other = gdn.make(Hk, H, d, d, [3, 1], seed=53)
+    at = make(4, 2, 64, [1, 1], [70, 9], seed=54)
+    sh, T = c["shape"], c["T"]
+    ws, wsb = gdn.workspace(c), torch.zeros(1 << 24, dtype=torch.uint8, device=DEV)
+    one = [x[:n].contiguous() for x in (c["q"], c["k"], c["v"], c["g"], c["beta"])]
+    mshape = abi.moe_shape(256, 128, 128, 16, 2, 4, 64)
+    x, wr = (torch.randn(r, 256, device=DEV).to(torch.bfloat16) for r in (20, 16))
+    idx, wts = torch.empty(20, 2, dtype=torch.int32, device=DEV), torch.empty(20, 2, device=DEV)
+    assert abi.moe_workspace_size(mshape, 20) <= wsb.numel()
+
+    def chain(flags):
+        S, S2, aside = c["S"].clone(), other["S"].clone(), other["S"].clone()
+        out = torch.zeros(T, H, d, dtype=torch.bfloat16, device=DEV)
+        outs = torch.zeros(rounds, 2, n, H, d, dtype=torch.bfloat16, device=DEV)
+        side_out, a_out = torch.zeros(4, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+
+        def calls():
+            st = torch.cuda.current_stream()
+            for r in range(rounds):
+                abi.moe_gdn_prefill(sh, n, T, c["off"], S, S, c["q"], c["k"], c["v"], c["g"], c["beta"], out, ws, stream=st)
+                for i in range(2):
+                    if between == "attention":
+                        abi.moe_attn_forward(at["shape"], 2, 2, at["off"], at["begin"], at["len"], at["max_kv"], at["q"], at["k"],
+                                             at["v"], at["rows"], at["scale"], a_out, wsb, stream=st)
+                    elif between == "prompt":
+                        abi.moe_gdn_prefill(sh, 2, 4, other["off"], other["S"], S2, other["q"], other["k"], other["v"], other["g"],
+                                            other["beta"], side_out, wsb, stream=st)
+                    elif between == "router":
+                        abi.moe_router_topk(mshape, x, 20, wr, None, idx, wts, wsb, stream=st)
+                    else:
+                        abi.moe_gdn_decode_step(sh, n, aside, *one, side_out, stream=st, flags=flags if i else 0)
+                    abi.moe_gdn_decode_step(sh, n, S, *one, outs[r, i], stream=st, flags=flags)
+
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if graph:
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=stream):
+                calls()
+            gr.replay()
+        else:
+            with torch.cuda.stream(stream):
+                calls()
+        torch.cuda.synchronize()
+        assert abi.moe_ws_check(ws) == 0 and abi.moe_ws_check(wsb) == 0
+        return S, out, outs
+
+    plain, early = chain(0), chain(abi.MOE_GDN_EARLY_STATE)
+    assert all(torch.equal(a, b) for a, b in zip(plain, early))
