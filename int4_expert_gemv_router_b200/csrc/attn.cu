@@ -1342,8 +1342,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
           *reinterpret_cast<uint2*>(dst) =
               u.seen + pos > 0 ? make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
         } else {
-          // a row's lanes are in one warp: they have all read the place that is overwritten
-          __syncwarp(__activemask());
+          // A row's lanes, all or half of a warp, have all read the place that is overwritten.  (The other
+          // half may be done: an odd number of rows.)
+          __syncwarp((kLanes == 32 ? 0xffffffffu : 0xffffu) << (lane & (32 - kLanes)));
           __stcg(reinterpret_cast<float4*>(a.part_o + at0 * D + c4), o);
           if (c4 == 0) __stcg(&a.part_ml[at0], make_float2(m, sum));
           __threadfence();

@@ -152,3 +152,14 @@ def test_early_state_reads_behind_a_kernel_that_writes_another(between, graph):
 
     plain, early = chain(0), chain(abi.MOE_GDN_EARLY_STATE)
     assert all(torch.equal(a, b) for a, b in zip(plain, early))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(5, 1, 64), (9, 1, 64), (30, 2, 64), (7, 1, 128)])
+def test_long_joins_of_an_odd_number_of_rows(Hq, Hkv, d):
+    """One token over keys in more than 16 pieces (joined in two steps), rows that fill no warp's halves."""
+    c = make(Hq, Hkv, d, [1, 0], [20000, 3], seed=55 + Hq)
+    out, ws = run(c)
+    assert abi.moe_ws_check(ws) == 0
+    check(c, out)
+    for _ in range(5):
+        assert torch.equal(run(c, ws)[0], out)
