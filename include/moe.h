@@ -418,6 +418,8 @@ typedef struct {
  *   scale     factor of the scores (finite), usually 1 / sqrt(d)
  *   out       (dev) bf16 [T, H_q, d] (round to nearest even)
  *   ws        (dev) workspace of ws_bytes >= moe_attn_workspace_size(shape, n_seqs, T, max_kv)
+ *             (which never falls as n_seqs, T or max_kv grows: one sized for a program's largest
+ *             numbers serves its smaller calls)
  * A query that sees no key (len < n) gets zeros.  Rows of out that belong to no sequence are
  * left as they were.  A sequence whose query rows are out of order or outside [0, T], or whose
  * keys lie outside [0, kv_rows) or number more than max_kv, is left out, its rows of out

@@ -1502,10 +1502,10 @@ struct AttnLayout {
   int PT, BP, rows_slot;
   bool few;
 };
-static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, int max_kv) {
+static AttnLayout attn_layout(const moe_attn_shape* shape, int n_seqs, int T, int max_kv, bool few) {
   AttnLayout W{};
   const int G = shape->n_q_heads / shape->n_kv_heads;
-  W.few = attn_few(shape, n_seqs, T);
+  W.few = few;
   W.PT = W.few ? kFewRows / G : kAttnTile / G;
   W.BP = W.few ? W.PT : 2 * W.PT;
   W.rows_slot = std::min(W.BP, std::max(T, 1)) * G;
@@ -1540,7 +1540,11 @@ extern "C" moe_status moe_attn_workspace_size(const moe_attn_shape* shape, int32
   const moe_status st = check_attn(shape, n_seqs, T, max_kv);
   if (st != MOE_OK) return st;
   if (!bytes) return set_error(MOE_ERR_INVALID, "bytes is NULL");
-  *bytes = attn_layout(shape, n_seqs, T, max_kv).total;
+  // Each kernel's layout grows with n_seqs, T and max_kv, but which kernel takes a call does not: fewer
+  // sequences of as many rows may need the larger layout.  The larger of both serves every smaller call.
+  *bytes = attn_layout(shape, n_seqs, T, max_kv, false).total;
+  if (shape->n_q_heads / shape->n_kv_heads <= kFewRows)
+    *bytes = std::max(*bytes, attn_layout(shape, n_seqs, T, max_kv, true).total);
   return MOE_OK;
 }
 
@@ -1561,7 +1565,7 @@ extern "C" moe_status moe_attn_forward(const moe_attn_shape* shape, int32_t n_se
   const uintptr_t all = (uintptr_t)q_offsets | (uintptr_t)kv_begin | (uintptr_t)kv_len | (uintptr_t)q | (uintptr_t)k |
                         (uintptr_t)v | (uintptr_t)out | (uintptr_t)ws;
   if (all & 15) return set_error(MOE_ERR_INVALID, "every pointer must be 16-byte aligned");
-  const AttnLayout W = attn_layout(shape, n_seqs, T, max_kv);
+  const AttnLayout W = attn_layout(shape, n_seqs, T, max_kv, attn_few(shape, n_seqs, T));
   if (ws_bytes < W.total) return set_error(MOE_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, W.total);
   if (T == 0) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);

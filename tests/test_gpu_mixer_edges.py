@@ -163,3 +163,17 @@ def test_long_joins_of_an_odd_number_of_rows(Hq, Hkv, d):
     check(c, out)
     for _ in range(5):
         assert torch.equal(run(c, ws)[0], out)
+
+
+def test_one_attention_workspace_for_every_smaller_call():
+    """Sized for the largest batch; fewer sequences with as many rows take another kernel and fit all the same."""
+    at = abi.moe_attn_shape(16, 2, 128)
+    size = abi.moe_attn_workspace_size(at, 64, 64, 4096)
+    ws = torch.zeros(size + 256, dtype=torch.uint8, device=DEV)
+    ws[size:] = 77
+    for lens, kv in (([1] * 64, [50 + 9 * i for i in range(64)]), ([64], [4096]), ([30, 34], [1000, 3000]), ([1], [4096])):
+        c = make(16, 2, 128, lens, kv, seed=56 + len(lens))
+        out, _ = run(c, ws[:size])
+        assert abi.moe_ws_check(ws) == 0
+        check(c, out, seqs=range(min(8, len(lens))))
+        assert (ws[size:] == 77).all()

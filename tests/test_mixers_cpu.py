@@ -121,3 +121,21 @@ def test_workspace_sizes_grow_and_refuse():
 
 def test_attn_without_queries_is_nothing():
     _attn(T=0, q=None)
+
+
+@pytest.mark.parametrize("shape", [(16, 2, 128), (16, 16, 64), (24, 2, 64), (64, 1, 128), (6, 2, 64)])
+def test_attn_workspace_never_falls(shape):
+    """Sized once for the largest numbers, it serves every smaller call."""
+    at = abi.moe_attn_shape(*shape)
+    size = {(n, T, kv): abi.moe_attn_workspace_size(at, n, T, kv)
+            for n in (1, 2, 3, 17, 64, 256, 1000) for T in (0, 1, 2, 16, 128, 512, 5000) for kv in (0, 1, 512, 513, 8192)}
+    for (n, T, kv), x in size.items():
+        for (m, U, kw), y in size.items():
+            assert not (n <= m and T <= U and kv <= kw) or x <= y, ((n, T, kv), (m, U, kw))
+
+
+def test_gdn_workspace_never_falls():
+    sh = abi.moe_gdn_shape(2, 4, 128, 64)
+    size = {(n, T): abi.moe_gdn_prefill_workspace_size(sh, n, T) for n in (1, 2, 63, 64, 65, 1000) for T in (0, 1, 63, 64, 65, 4000)}
+    for (n, T), x in size.items():
+        assert all(x <= y for (m, U), y in size.items() if n <= m and T <= U)
