@@ -375,8 +375,9 @@ MOE_API moe_status moe_gdn_decode_step_ex(const moe_gdn_shape* shape, int32_t B,
  * 4 d_k H_k + 270 H_v bytes per token.  Rows of out that belong to no sequence are left as they
  * were.  A sequence whose range is out of order or outside [0, T] (offsets[s+1] < offsets[s],
  * offsets[s+1] > T, or offsets[s] below an earlier offset) is left out, its rows of out and
- * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  An infinity or NaN in a token's
- * inputs reaches the tokens behind it, and may reach those before it in its chunk of 64 tokens.
+ * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  An infinity or NaN reaches what it
+ * reaches in the steps: in q its own token, in v its column from that token on, in k, g or beta (but
+ * g = -inf) the heads that read it from that token on, and no token before it.
  * Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_gdn_prefill_workspace_size(const moe_gdn_shape* shape, int32_t n_seqs, int32_t T,

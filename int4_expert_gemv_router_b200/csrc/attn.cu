@@ -468,7 +468,6 @@ __device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, int idx, const 
 // Rows behind the sequence's last key, which hold anything, are cleared.  Tiles whose keys every row
 // sees need none of it.  (Looking through those tiles beside their softmax: ragged prompts 89.6 -> 91.9 us,
 // pieces 77.1 -> 78.5, the 16,384-token prompt and single tokens unchanged.)
-__device__ __forceinline__ uint32_t bf16x2_nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 // Rows first .. n - 1 of a value tile in shared memory (64-column boxes of 128-byte rows): rows from `len`
 // on cleared, non-finite elements of the others replaced by 0 where `scan`.  A whole warp; true in a
 // lane that replaced one.

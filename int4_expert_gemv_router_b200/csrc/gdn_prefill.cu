@@ -76,7 +76,8 @@ struct GdnTP {
   float wd[kGdnChunk];               // e^{G_64 - G_i} / |k_i|, over `wd_scale`
   float keep;                        // e^{G_64}
   float t_scale, p_scale, wd_scale;  // what t, p and wd are to be multiplied by (powers of two but p's)
-  float pad[60];
+  int plain;                         // the chunk is to be done token by token (see gdn_scan)
+  float pad[59];
 };
 static_assert(sizeof(GdnTP) % 256 == 0, "bulk copies; V behind it starts on a period of its swizzle");
 // Block of token tile t (8 tokens) and step k (16 tokens), k <= t / 2
@@ -264,21 +265,32 @@ __device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
   down = __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
+// (NaN if one is)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Accumulators of N tiles of 8 columns (rows g and g + 8 of a slab) -> the largest element of
-// each of the two rows over the warp's columns.
+// each of the two rows over the warp's columns; NaN if one is.
 template <int N>
 __device__ __forceinline__ void row_max(const float2 (&v)[N][2], float (&m)[2]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float x[2] = {0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < N; ++t) x[t & 1] = fmaxf(x[t & 1], fmaxf(fabsf(v[t][e].x), fabsf(v[t][e].y)));
-    m[e] = fmaxf(x[0], x[1]);
+    for (int t = 0; t < N; ++t) x[t & 1] = max_nan3(x[t & 1], fabsf(v[t][e].x), fabsf(v[t][e].y));
+    m[e] = max_nan(x[0], x[1]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-    m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+    m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    m[1] = max_nan(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
   }
 }
 // x = hi + lo in fp16, as A operands: a step of 16 columns takes the registers of two tiles
@@ -403,7 +415,9 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
   __shared__ float2 s_G[2][kGdnChunk];  // log2(e) G_i, as two floats
   __shared__ float s_pm[2];             // the largest G_i - G_j, j <= i (0 where nothing grows)
   __shared__ float s_red[2][6];
+  __shared__ int s_plain[3];            // a head's decays or writes, or the keys, ask for single tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_plain[2] = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int chunk = blockIdx.x / a.Hk, kh = blockIdx.x - chunk * a.Hk;
@@ -481,6 +495,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
       for (int e = 0; e < 4; ++e) {
         const uint32_t w = word_of(piece[i], e);
         h[e] = pack_h2(mul2(make_float2(bf_lo(w), bf_hi(w)), both(up)));
+        if (up == 0.f && i < N / 2 && bf16x2_nonfinite(w)) s_plain[2] = 1;  // (rows of a finite norm have none)
       }
       const int at = r * LPR + (col ^ (row & 7));
       const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]);
@@ -492,12 +507,15 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
   // clamped, e^-1e4 = 0), kept as two floats, in units of log 2; one warp per head
   auto decays = [&](int h) {
     double x[2];
+    bool bad = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int t = 2 * lane + e;
       const float gt = t < C.n ? a.g[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+      const float bt = t < C.n ? a.beta[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
       x[e] = (gt < -1e4f ? -1e4 : (double)gt) * 1.4426950408889634;
-      s_beta[team][t] = t < C.n ? a.beta[(size_t)(C.row0 + t) * a.Hv + h] : 0.f;
+      s_beta[team][t] = bt;
+      bad |= !(gt < INFINITY) || !(fabsf(bt) < INFINITY);
     }
     double sum = x[0] + x[1];
 #pragma unroll
@@ -519,7 +537,11 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
     float up = (float)fmax(lane ? g0 - fmin(before, g0) : 0.0, g1 - low);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-    if (lane == 0) s_pm[team] = up;
+    bad = __any_sync(0xffffffffu, bad) || up > 126.f;  // (a growth that fp32 does not hold)
+    if (lane == 0) {
+      s_pm[team] = up;
+      s_plain[team] = bad;
+    }
   };
   if (tw == 0 && team < rep) decays(kh * rep + team);
   __syncthreads();
@@ -619,7 +641,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
             }
             v[y][k][e] = x.x;
             v[y][k][e + 1] = x.y;
-            m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+            m = max_nan3(m, fabsf(x.x), fabsf(x.y));
           }
       }
       if (tt < kGdnChunk) {
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
       float mw = wd;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
       }
       if (lane == 0) {
@@ -641,7 +663,8 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
       }
       team_sync(team);
       float up, down, upw, downw;
-      pow2_scale<14>(fmaxf(fmaxf(s_red[team][0], s_red[team][1]), fmaxf(s_red[team][2], s_red[team][3])), up, down);
+      const float t_max = max_nan(max_nan(s_red[team][0], s_red[team][1]), max_nan(s_red[team][2], s_red[team][3]));
+      pow2_scale<14>(t_max, up, down);
       pow2_scale<0>(fmaxf(s_red[team][4], s_red[team][5]), upw, downw);
       if (tt < kGdnChunk) tp->wd[tt] = wd * upw;
       if (tt == 0) {
@@ -649,6 +672,8 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
         tp->t_scale = down;
         tp->p_scale = ex2f(pm) * 0x1p-10f;
         tp->wd_scale = downw;
+        // (the rule contracts for 0 <= beta <= 2: |T'| <= 4; far above it the writes could overflow)
+        tp->plain = s_plain[team] | s_plain[2] | !(t_max < 0x1p64f);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -688,6 +713,82 @@ __device__ __forceinline__ void slab_sync(int slab, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(slab + 1), "r"(threads) : "memory");
 }
 __device__ __forceinline__ float4 cat(const float2 (&d)[2]) { return make_float4(d[0].x, d[0].y, d[1].x, d[1].y); }
+
+// Chunk c of a slab, its tokens one by one in fp32, as the decode step does them (k_gdn_step): for chunks
+// with infinities or NaN, which then reach the tokens behind them alone.  All of the slab's warps call it;
+// xch: its exchange area.  (1.6 us a token, where the chunk takes 3 us in one go; that every chunk can come
+// here costs the others 1 to 2 %: 16 x 1024 tokens 549 -> 562 us, 1 x 8192 437 -> 441.)
+template <int DK, int NS>
+__device__ __forceinline__ void gdn_tokens(const GdnPrefillArgs& a, const GdnSeq seq, int c, int h, int vr, int slab, int w,
+                                           float2 (&S)[NS * 8][2], float* xch) {
+  constexpr int NW = DK / (kGdnSlice * NS);
+  const int lane = threadIdx.x & 31, g = lane >> 2, u = 2 * (lane & 3), kh = h / (a.Hv / a.Hk);
+  const auto slab_sum = [&](float (&x)[2], float* at) {  // over the columns of rows g and g + 8
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+      x[1] += __shfl_xor_sync(0xffffffffu, x[1], o);
+    }
+    if constexpr (NW > 1) {
+      if ((lane & 3) == 0) {
+        at[w * kGdnSlab + g] = x[0];
+        at[w * kGdnSlab + g + 8] = x[1];
+      }
+      slab_sync(slab, NW * 32);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[e] = at[g + 8 * e];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) x[e] += at[v * kGdnSlab + g + 8 * e];
+      }
+    }
+  };
+  for (int i = 0; i < min(kGdnChunk, seq.n - c * kGdnChunk); ++i) {
+    const size_t row = (size_t)seq.row0 + c * kGdnChunk + i;
+    float2 x[2][NS * 8];  // k^, q^: this lane's columns
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint16_t* src = (z ? a.q : a.k) + (row * a.Hk + kh) * DK;
+      float ss = 0.f;
+      for (int j = 2 * lane; j < DK; j += 64) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(src + j);
+        ss = fmaf(bf_lo(v), bf_lo(v), fmaf(bf_hi(v), bf_hi(v), ss));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = 1.0f / fmaxf(sqrtf(ss), 1e-6f) * (z ? rsqrtf((float)DK) : 1.f);
+#pragma unroll
+      for (int t = 0; t < NS * 8; ++t) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(src + w * NS * kGdnSlice + t * 8 + u);
+        x[z][t] = make_float2(bf_lo(v) * inv, bf_hi(v) * inv);
+      }
+    }
+    const float alpha = expf(a.g[row * a.Hv + h]), beta = a.beta[row * a.Hv + h];
+    float r[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < NS * 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) r[e] = fmaf(S[t][e].x, x[0][t].x, fmaf(S[t][e].y, x[0][t].y, r[e]));
+    slab_sum(r, xch);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float v = vr + 8 * e < a.dv ? bf1(a.v[(row * a.Hv + h) * a.dv + vr + 8 * e]) : 0.f;
+      const float f = beta * (v - alpha * r[e]);
+#pragma unroll
+      for (int t = 0; t < NS * 8; ++t) {
+        S[t][e].x = fmaf(alpha, S[t][e].x, f * x[0][t].x);
+        S[t][e].y = fmaf(alpha, S[t][e].y, f * x[0][t].y);
+        o[e] = fmaf(S[t][e].x, x[1][t].x, fmaf(S[t][e].y, x[1][t].y, o[e]));
+      }
+    }
+    slab_sum(o, xch + NW * kGdnSlab);
+    if (w == 0 && (lane & 3) == 0)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (vr + 8 * e < a.dv) a.out[(row * a.Hv + h) * a.dv + vr + 8 * e] = f2bf(o[e]);
+  }
+  if constexpr (NW > 1) slab_sync(slab, NW * 32);  // the area is the next chunk's again
+}
 
 // One CTA's slabs of one sequence and value head: state rows rb * slabs * 16 and on.
 template <int DK, int NS>
@@ -757,13 +858,19 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
   }
 
   bool ok = true;
+  bool plain = false;  // this slab has left the chunk before undone (every warp of a slab says the same)
   int issued = 0;
   if (n_ch > 0) load(issued++);
-  for (int c = 0; c < n_ch; ++c) {
+  for (int c = 0;; ++c) {
     // everyone is done with the other stage and with the exchange area (and the plain stores of
     // this chunk's V are visible)
-    ok = __syncthreads_and(ok);
-    if (!ok) break;
+    if (__syncthreads_or(!ok || plain)) {
+      ok = !__syncthreads_or(!ok);
+      if (!ok) break;
+      if (plain) gdn_tokens<DK, NS>(a, seq, c - 1, h, vr, slab, w, S, reinterpret_cast<float*>(smem + 2 * stage_bytes + slab * M::kXch));
+      plain = false;
+    }
+    if (c == n_ch) break;
     if (c + 1 < n_ch) load(issued++);
     ok = mbar_wait(&full[c & 1], (c >> 1) & 1);
     const uint32_t st = smem_u32(smem) + (c & 1) * stage_bytes;
@@ -876,6 +983,19 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
     {
       float m[2], up[2], dn[2];
       row_max(X, m);
+      // An infinity or NaN in one token's R would reach the tokens before it (as 0 times it, and through
+      // the row's scale): the slab then does the chunk's tokens one by one, behind the next barrier.  Not
+      // where the row's first R is one already (a state that holds one): all of the row becomes NaN.
+      if (__any_sync(0xffffffffu, tp->plain || !(max_nan(m[0], m[1]) < INFINITY))) {
+        bool need = tp->plain;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float first = __shfl_sync(0xffffffffu, X[0][e].x, lane & 28);  // (every lane takes part)
+          need |= !(m[e] < INFINITY) && fabsf(first) < INFINITY;
+        }
+        plain = __any_sync(0xffffffffu, need);
+        if (plain) continue;
+      }
       pow2_scale<14>(m[0], up[0], dn[0]);
       pow2_scale<14>(m[1], up[1], dn[1]);
       uint32_t hi[8][2], lo[8][2];
@@ -1011,7 +1131,6 @@ __device__ __forceinline__ void gdn_scan(const GdnPrefillArgs& a, const int slab
       }
     }
   }
-  ok = __syncthreads_and(ok);
   if (!ok) {  // a copy never landed: no state is written, and the copies in flight are waited for
     if (tid == 0) atomicOr(&a.ctrl->err, kErrTimeout);
     for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait(&full[c & 1], (c >> 1) & 1);

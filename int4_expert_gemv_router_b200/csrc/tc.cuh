@@ -94,6 +94,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Bits 15 and 31: the low and the high one of two bf16 are infinite or NaN.
+__device__ __forceinline__ uint32_t bf16x2_nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
 __device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, Ctrl* c) {
   if (mbar_wait_suspend(bar, parity)) return true;
   atomicOr(&c->err, kErrTimeout);

@@ -177,3 +177,73 @@ def test_one_attention_workspace_for_every_smaller_call():
         assert abi.moe_ws_check(ws) == 0
         check(c, out, seqs=range(min(8, len(lens))))
         assert (ws[size:] == 77).all()
+
+
+def prompt_reference(c):
+    """The recurrence in 64 bits with whatever the inputs hold (the normalised keys of a row with an infinity
+    or NaN are not finite either)."""
+    sh, off = c["shape"], c["off"].tolist()
+    rep, outs, states = sh.n_v_heads // sh.n_k_heads, [], []
+    for s in range(c["n"]):
+        S = torch.zeros(sh.n_v_heads, sh.d_v, sh.d_k, device=DEV, dtype=torch.float64) if c["S"] is None else c["S"][s].double()
+        for t in range(off[s], off[s + 1]):
+            k, q = (x[t].double() for x in (c["k"], c["q"]))
+            k, q = (x / x.square().sum(-1, keepdim=True).sqrt().clamp_min(1e-6) for x in (k, q))
+            k, q = k.repeat_interleave(rep, 0)[:, None], q.repeat_interleave(rep, 0)[:, None] / sh.d_k ** 0.5
+            S = S * c["g"][t].double().exp()[:, None, None]
+            S = S + (c["beta"][t].double()[:, None] * (c["v"][t].double() - (S * k).sum(-1)))[..., None] * k
+            outs.append((S * q).sum(-1))
+        states.append(S)
+    return torch.stack(outs), torch.stack(states)
+
+
+NONFINITE = [  # (input, token, value head or key head, column, value); tokens count over the call
+    [("v", 100, 1, 7, float("inf"))], [("v", 100, 1, 7, float("nan"))], [("v", 0, 0, 0, -float("inf"))],
+    [("v", 149, 3, 2, float("nan")), ("v", 20, 2, 3, float("inf"))], [("v", 64, 0, 1, float("inf"))],
+    [("k", 70, 0, 3, float("nan"))], [("k", 63, 1, 60, -float("inf"))], [("q", 90, 1, 5, float("nan"))],
+    [("q", 0, 0, 0, float("inf"))], [("g", 33, 1, None, float("nan"))], [("g", 99, 2, None, float("inf"))],
+    [("beta", 127, 0, None, float("nan"))], [("beta", 1, 3, None, float("inf"))],
+    [("S", 0, 2, 9, float("inf"))], [("S", 1, 0, 0, float("nan"))],  # the start of sequence 0 or 1
+    [("g", 40, 1, None, -float("inf")), ("v", 30, 1, 4, float("nan"))],  # forgetting does not bring it back
+]
+
+
+@pytest.mark.parametrize("bad", NONFINITE, ids=lambda b: "-".join(f"{x[0]}{x[1]}" for x in b))
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(2, 4, 128, 40), (2, 4, 64, 33), (2, 4, 256, 24), (2, 96, 128, 128), (2, 64, 256, 96)])
+def test_prompt_infinities_and_nan_reach_the_tokens_behind_them(Hk, Hv, dk, dv, bad):
+    """... of their sequence, head and (a value's) column, and nothing else: the rest stays within the bars
+    of the same call without them.  The shapes take one and two slices a warp, and one to four warps a slab."""
+    c = gdn.make(Hk, Hv, dk, dv, [150, 70], seed=57)
+    clean = dict(c)
+    c = dict(c, **{x: c[x].clone() for x in ("q", "k", "v", "g", "beta", "S")})
+    for name, t, h, col, val in bad:
+        if name == "S":
+            c["S"][t, h, col % dv, col] = val
+        elif col is None:
+            c[name][t, h] = val
+        else:
+            c[name][t, h, col] = val
+    want, S_want = prompt_reference(c)
+    out, S, ws = gdn.run(c)
+    assert abi.moe_ws_check(ws) == 0
+    base, S_base, _ = gdn.run(clean, ws=ws)
+    gdn.check(clean, base, S_base)
+    finite, S_finite = torch.isfinite(want), torch.isfinite(S_want)
+    assert not finite.all() and finite.any() and torch.equal(torch.isfinite(out.float()), finite)
+    assert torch.equal(torch.isfinite(S), S_finite)
+    # within the bars of the clean call where the oracle's sizes are (they do not depend on what was planted)
+    off = clean["off"].tolist()
+    for s in range(2):
+        at = slice(off[s], off[s + 1])
+        S_ref, o, size, m = gdn.oracle.gdn_prompt(clean["S"][s].double().cpu().numpy(), *(gdn.f64(clean[x][at]) for x in "qkv"),
+                                                  *(clean[x][at].double().cpu().numpy() for x in ("g", "beta")))
+        o, size, m, S_ref = (torch.from_numpy(x).to(DEV) for x in (o, size, m, S_ref))
+        ok = (out[at].double() - want[at]).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -10) * size + 1e-36
+        assert ok[finite[at]].all()
+        assert ((S[s].double() - S_want[s]).abs() <= 2.0 ** -14 * m[..., None])[S_finite[s]].all()
+    # the same call, the same bits; and the sequence without any keeps its own
+    again, S_again, _ = gdn.run(c, ws=ws)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(S.view(torch.int32), S_again.view(torch.int32))
+    for s in range(2):
+        if finite[off[s]:off[s + 1]].all():
+            assert torch.equal(out[off[s]:off[s + 1]], base[off[s]:off[s + 1]]) and torch.equal(S[s], S_base[s])
