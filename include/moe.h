@@ -378,6 +378,9 @@ MOE_API moe_status moe_gdn_decode_step_ex(const moe_gdn_shape* shape, int32_t B,
  * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  An infinity or NaN reaches what it
  * reaches in the steps: in q its own token, in v its column from that token on, in k, g or beta (but
  * g = -inf) the heads that read it from that token on, and no token before it.
+ * The state stays fp32; products take operands of 22 bits, and where only out depends on them 11.
+ * What a state row has written in 64 tokens shares one scale: a write below 2^-18 of the row's
+ * largest there is good to 2^-30 of that largest instead.
  * Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_gdn_prefill_workspace_size(const moe_gdn_shape* shape, int32_t n_seqs, int32_t T,

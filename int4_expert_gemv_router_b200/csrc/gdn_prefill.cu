@@ -29,8 +29,13 @@
 // K is exact: its rows, scaled by powers of two to a norm of 2^10 .. 2^11, fit fp16 (bf16 has
 // fewer bits), and the norm's factor is applied in fp32.  S, R and W are split x = hi + lo into two
 // fp16 values after scaling each row by a power of two to its largest element: 22 bits of the row's
-// size; T' likewise by its rows.  S K^T and W K take two products (hi, lo), T' R three (lo lo is
-// below 2^-22).  What only the bf16 output sees (Q S, P W) takes hi alone, 2^-12 of each weight.
+// size; T' likewise by its largest element.  S K^T and W K take two products (hi, lo), T' R three (lo lo
+// is below 2^-22).  What only the bf16 output sees (Q S, P W) takes hi alone, 2^-12 of each weight.
+// The scale is a row's over the chunk, and fp16 ends at 2^-24: an element below 2^-18 of its row's
+// largest in the 64 tokens keeps 2^-39 of that largest, not 22 bits of its own.  Sums of 64 of them are
+// good to 2^-30 of it, which can only show where a decay inside the chunk (or the order of the tokens)
+// parts writes that are more than 2^16 apart.  A scale of each token's own would have to be undone in T',
+// whose entries are shared by all rows.
 // mma.sync carries this, not tcgen05: the slab's products are 16 rows high, 8 to 64 wide and
 // dependent on each other, and a chunk's chain of six of them through TMEM (a round trip of
 // registers, TMEM, MMA and back for each) costs more than the products themselves.
@@ -329,7 +334,9 @@ __device__ __forceinline__ void team_sync(int team) {
 }
 
 // d (16 x 8, fp32) += a (16 x 8) b (8 x 8), both fp32 in shared memory with rows of kMatLd, as the
-// products of their tf32 heads and rests (rest times rest is below 2^-22).
+// products of their tf32 heads and rests.  A head is cut off after 10 bits, so a rest is below 2^-10 of its
+// element, and the tensor core takes 10 bits of it: rest times rest, and the rests' ends, are below 2^-20 of
+// a product.
 __device__ __forceinline__ void tf32_parts(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;  // 10 mantissa bits: exact in tf32
   lo = __float_as_uint(x - __uint_as_float(hi));

@@ -247,3 +247,27 @@ def test_prompt_infinities_and_nan_reach_the_tokens_behind_them(Hk, Hv, dk, dv, 
     for s in range(2):
         if finite[off[s]:off[s + 1]].all():
             assert torch.equal(out[off[s]:off[s + 1]], base[off[s]:off[s + 1]]) and torch.equal(S[s], S_base[s])
+
+
+@pytest.mark.parametrize("big", [2.0 ** 10, 2.0 ** 20, 2.0 ** 30, 1e20])
+@pytest.mark.parametrize("order", ["forgotten", "later"])
+def test_writes_far_apart_in_one_chunk(order, big):
+    """Values `big` times the others' in some columns at one token of a chunk, which a decay then forgets,
+    or which comes last.  What shares a scale is good to 2^-30 of the row's largest write in the chunk:
+    fp16 pairs of elements scaled to 2^13 .. 2^15 step by 2^-24, so by at most 2^-38 of the largest, in
+    R, in T' (whose row meets up to 64 of them) and in W (whose column does): 3 * 64 * 2^-38 < 2^-30.
+    The bars of ordinary inputs come on top."""
+    c = gdn.make(2, 4, 128, 48, [64], seed=58)
+    t = 10 if order == "forgotten" else 60
+    c["v"][t, :, 5:9] *= big
+    if order == "forgotten":
+        c["g"][t + 1] = -float("inf")
+    out, S, ws = gdn.run(c)
+    assert abi.moe_ws_check(ws) == 0
+    S_ref, o, size, m = gdn.oracle.gdn_prompt(c["S"][0].double().cpu().numpy(), *(gdn.f64(c[x]) for x in "qkv"),
+                                              *(c[x].double().cpu().numpy() for x in ("g", "beta")))
+    top = size.max(0)  # over the chunk
+    bar = 2.0 ** -8 * abs(o) + (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -30 * top
+    assert (abs(gdn.f64(out) - o) <= bar).all()
+    bar = 2.0 ** -14 * m + 2.0 ** -30 * top * 128 ** 0.5
+    assert (abs(S[0].double().cpu().numpy() - S_ref) <= bar[..., None]).all()
