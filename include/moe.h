@@ -371,9 +371,10 @@ MOE_API moe_status moe_gdn_decode_step_ex(const moe_gdn_shape* shape, int32_t B,
  *   beta       (dev) fp32 [T, H_v]
  *   out        (dev) bf16 [T, H_v, d_v] (round to nearest even of the fp32 value)
  *   ws         (dev) workspace of ws_bytes >= moe_gdn_prefill_workspace_size(shape, n_seqs, T)
- * Shapes as moe_gdn_decode_step.  The workspace holds what each 64-token chunk needs, about
- * 4 d_k H_k + 270 H_v bytes per token.  Rows of out that belong to no sequence are left as they
- * were.  A sequence whose range is out of order or outside [0, T] (offsets[s+1] < offsets[s],
+ * Shapes as moe_gdn_decode_step.  The workspace holds what each chunk of 64 tokens needs, 256 d_k H_k +
+ * 16,384 H_v + 8 bytes for each of up to T / 64 + min(n_seqs, T) chunks (every sequence has a ragged
+ * one), beside 16 bytes a sequence; it never falls as n_seqs or T grows.  Rows of out that belong to no
+ * sequence are left as they were.  A sequence whose range is out of order or outside [0, T] (offsets[s+1] < offsets[s],
  * offsets[s+1] > T, or offsets[s] below an earlier offset) is left out, its rows of out and
  * its state_out untouched, and MOE_DEVERR_BAD_RANGE is set.  An infinity or NaN reaches what it
  * reaches in the steps: in q its own token, in v its column from that token on, in k, g or beta (but

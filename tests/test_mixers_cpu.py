@@ -139,3 +139,13 @@ def test_gdn_workspace_never_falls():
     size = {(n, T): abi.moe_gdn_prefill_workspace_size(sh, n, T) for n in (1, 2, 63, 64, 65, 1000) for T in (0, 1, 63, 64, 65, 4000)}
     for (n, T), x in size.items():
         assert all(x <= y for (m, U), y in size.items() if n <= m and T <= U)
+
+
+@pytest.mark.parametrize("n,T", [(1, 64), (1, 8192), (16, 16 * 1024), (4096, 4096), (10, 3678), (3, 0)])
+def test_gdn_workspace_is_what_the_header_states(n, T):
+    """256 d_k H_k + 16,384 H_v + 8 bytes a chunk, T / 64 + min(n_seqs, T) chunks, 16 bytes a sequence, the
+    control block and each part's padding to 256 bytes."""
+    Hk, Hv, dk = 16, 32, 128
+    stated = (T // 64 + min(n, T)) * (256 * dk * Hk + 16384 * Hv + 8) + 16 * n
+    got = abi.moe_gdn_prefill_workspace_size(abi.moe_gdn_shape(Hk, Hv, dk, 128), n, T)
+    assert stated <= got <= stated + 8 * 256 + 256
