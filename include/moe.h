@@ -400,7 +400,7 @@ typedef struct {
   int32_t n_q_heads;   /* H_q: query heads                                                   */
   int32_t n_kv_heads;  /* H_kv: key/value heads (query head h reads key head                 */
                        /*       h / (H_q / H_kv); H_q / H_kv a whole number up to 64)        */
-  int32_t d;           /* head width: 64 or 128                                              */
+  int32_t d;           /* head width: 64 or 128 (others: MOE_ERR_UNSUPPORTED)                */
 } moe_attn_shape;
 
 /*
@@ -430,7 +430,12 @@ typedef struct {
  * keys lie outside [0, kv_rows) or number more than max_kv, is left out, its rows of out
  * untouched, and MOE_DEVERR_BAD_RANGE is set.  Sequences may share keys.  An infinity or NaN in
  * a key or its value reaches the queries that see the key and no others (an infinite value as
- * an infinity or NaN).  Deterministic: the same call gives the same bits.
+ * an infinity or NaN).  T = 0 returns at once: nothing is enqueued and no range is looked at.
+ * Scores, maxima and sums are fp32.  The weights meet the values rounded to bf16, half a step (2^-8)
+ * of each weight, in calls of many rows, and as two bf16 values (2^-16) in calls of few: those with
+ * H_q / H_kv <= 16 and T H_q / H_kv <= 16 n_seqs.  That rule sees the mean only, and the few-rows
+ * kernel reads a sequence's keys once per 16 rows: leave empty slots out of a call that has prompts.
+ * Deterministic: the same call gives the same bits.
  */
 MOE_API moe_status moe_attn_workspace_size(const moe_attn_shape* shape, int32_t n_seqs, int32_t T, int32_t max_kv,
                                            size_t* bytes);
