@@ -70,7 +70,6 @@ struct AttnHdr {
 };
 
 constexpr int kAttnTile = 128;     // rows of a query tile and of a key tile
-constexpr int kAttnRound = 148;    // a unit for every SM
 constexpr int kAttnFill = 222;     // pieces that keys are cut for (tile kernel; pieces after histories: 148 71.2 us, 222 66.8, 296 68.9)
 constexpr int kAttnFillFew = 296;  // and for few rows
 constexpr int kAttnMinPiece = 4;   // key tiles of a piece at least
@@ -84,6 +83,7 @@ struct AttnArgs {
   int fill;          // pieces that keys are cut for; 0: nothing is cut
   int sort;          // units in order, longest first
   int few;           // the few-rows kernel's call
+  int n_sm;
   int self_plan;     // no plan kernel: every CTA finds its one unit for itself
   float scale_log2;  // scale * log2(e)
   const int32_t *offsets, *kv_begin, *kv_len;
@@ -164,17 +164,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const __grid_constan
       atomicAdd(&s_blocks, blocks);
     }
     __syncthreads();
-    // Few blocks (U of them over the key heads): at most W / P + U <= kAttnRound pieces, one round of
-    // the SMs (one token over 60,001 keys 37 -> 29 us, against 296).
+    // Few blocks (U of them over the key heads): at most W / P + U <= n_sm pieces, one round of the SMs
+    // (one token over 60,001 keys 37 -> 29 us, against 296).
     const float U = (float)s_blocks * (float)a.Hkv, work_all = (float)s_work * (float)a.Hkv;
-    const bool round = 2.f * U <= kAttnRound;
+    const bool round = 2.f * U <= a.n_sm;
     const auto tiles = [](float per) {  // rounded up, and never below the quotient
       return per < 1e7f ? max(kAttnMinPiece, (int)(per * 1.0001f + 0.9999f)) : 1 << 24;
     };
-    P = tiles(work_all / (round ? kAttnRound - U : a.fill));
+    P = tiles(work_all / (round ? a.n_sm - U : a.fill));
     // A block of no more key tiles than an SM's share is not in the way of the others: cut all the same,
     // its partial results only cost (ragged prompts 101.6 us, whole 90.2).
-    longest = round || a.few ? P : tiles(work_all / kAttnRound);
+    longest = round || a.few ? P : tiles(work_all / min(a.n_sm, a.fill));
   }
   // Place the units; longest first (a counting sort, two rounds) where a CTA has several.
   const float to_bin = (float)(kPlanThreads - 1) / (float)(a.fill ? longest : max(1, (a.max_kv + kAttnTile - 1) / kAttnTile));
@@ -289,21 +289,9 @@ struct AttnSmem {
   static constexpr int kBytes = (2 + kStages) * kTile + 1024;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float2 fadd2p(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
   return d;
 }
 
@@ -686,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn(const __grid_constant_
             const float2 e = ffma2(make_float2(__uint_as_float(sv[0]), __uint_as_float(sv[1])), make_float2(sl, sl),
                                    make_float2(ms, ms));
             const float2 pv = make_float2(ex2(e.x), ex2(e.y));
-            sum[i & 1] = fadd2p(sum[i & 1], pv);
+            sum[i & 1] = add2(sum[i & 1], pv);
             p[i] = pack_bf16(pv.x, pv.y);
           }
           tmem_st32(t_s + h * kHalf, p);
@@ -996,18 +984,6 @@ struct FewSmem {
   static constexpr int kBytes = kStages * 2 * kTile + 2 * kSum + 1024;
 };
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 // d (16 x 8, fp32) += a (16 x 16, bf16) b (16 x 8, bf16); fragments as in the PTX manual
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -1242,7 +1218,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_attn_few(const __grid_consta
           for (int r = 0; r < 2; ++r) {
             float2* at = reinterpret_cast<float2*>(mine + (g + 8 * r) * L::kLd + n * 8 + u2);
             float2 v = make_float2(O[n][2 * r], O[n][2 * r + 1]);
-            if (turn) v = fadd2p(v, *at);
+            if (turn) v = add2(v, *at);
             *at = v;
           }
       }
@@ -1434,6 +1410,7 @@ static cudaError_t launch_attn_d(AttnArgs& a, const uint16_t* q, bool few, int n
   // thousand: 38.5 against 36.3)
   a.sort = units > n_sm && !(few && blocks * a.Hkv <= 2 * n_sm);
   a.few = few;
+  a.n_sm = std::min(n_sm, kAttnMaxSlots);  // (pieces of one round have a slot each)
   a.self_plan = a.n_seqs <= kWarpSeqs && !cut && units <= n_sm;
   cudaError_t e = a.self_plan ? cudaSuccess : launch_pdl(k_attn_plan, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;

@@ -213,18 +213,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const GdnPrefillArgs 
   }
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 // d (16 x 8, fp32) += a (16 x 16, fp16) b (16 x 8, fp16); mma16z: d = a b.  With g = lane / 4,
 // u = 2 (lane % 4): d[0] = row g, columns u, u + 1, d[1] = row g + 8; a0 = (g, u..), a1 = (g + 8, u..),
 // a2 = (g, u + 8..), a3 = (g + 8, u + 8..); b0 = (k u.., n g), b1 = (k u + 8.., n g).
@@ -248,13 +236,6 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
       : "=l"(reinterpret_cast<unsigned long long&>(d))
       : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
   return d;
@@ -321,13 +302,8 @@ struct GdnChunkSmem {
   static constexpr int kBytes = kFirst + 2 * kMat;
 };
 
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 2^(a - b) of sums held as two floats: the difference of the heads is exact or as good as its size
-__device__ __forceinline__ float decay(float2 a, float2 b) { return ex2f((a.x - b.x) + (a.y - b.y)); }
+__device__ __forceinline__ float decay(float2 a, float2 b) { return ex2((a.x - b.x) + (a.y - b.y)); }
 
 __device__ __forceinline__ void team_sync(int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kHeadThreads) : "memory");
@@ -389,7 +365,7 @@ __device__ __forceinline__ void join_blocks(float* C, const float* A, const floa
 // (I + L)^-1 in place of the strictly lower triangular L (zeros elsewhere), by a team of 128
 // threads: the four 16 x 16 diagonal blocks by forward substitution, a thread a column, then
 // joined to blocks of 32 and of 64 on the tensor cores (on the FMA units the joins were bound by
-// shared-memory reads, 272 instead of 255 us for the 16,384 tokens and 32 heads of a batch).
+// shared-memory reads: 17 us more for the 16,384 tokens and 32 heads of a batch).
 __device__ __forceinline__ void invert(float* L, int t, int team) {
   if (t < kGdnChunk) {
     const int b = t / 16, j = t % 16;
@@ -677,7 +653,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
       if (tt == 0) {
         tp->keep = decay(s_G[team][kGdnChunk - 1], make_float2(0.f, 0.f));
         tp->t_scale = down;
-        tp->p_scale = ex2f(pm) * 0x1p-10f;
+        tp->p_scale = ex2(pm) * 0x1p-10f;
         tp->wd_scale = downw;
         // (the rule contracts for 0 <= beta <= 2: |T'| <= 4; far above it the writes could overflow)
         tp->plain = s_plain[team] | s_plain[2] | !(t_max < 0x1p64f);
