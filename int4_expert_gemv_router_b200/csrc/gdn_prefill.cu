@@ -291,6 +291,11 @@ __device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
 // ---------------------------------------------------------------------------------------
 constexpr int kChunkThreads = 256;  // four warps per value head, two value heads at a time
 constexpr int kHeadThreads = 128;
+// log2 of how far a state may grow in a chunk (g > 0).  P is held relative to the largest factor, in fp16
+// times 2^10, and a row's W relative to its largest token: what comes before a growth of 2^16 still has
+// steps of 2^-19 and 2^-22 of its own size, and loses a bit with every doubling.  Beyond it the tokens
+// go one by one.
+constexpr float kMaxGrowth = 16.f;
 constexpr int kMatLd = 68;          // row stride (floats) of the 64 x 64 matrices: 16-byte rows
 
 template <int DK>
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
     float up = (float)fmax(lane ? g0 - fmin(before, g0) : 0.0, g1 - low);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-    bad = __any_sync(0xffffffffu, bad) || up > 126.f;  // (a growth that fp32 does not hold)
+    bad = __any_sync(0xffffffffu, bad) || up > kMaxGrowth;
     if (lane == 0) {
       s_pm[team] = up;
       s_plain[team] = bad;
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
       team_sync(team);
       invert(L, tt, team);
       // P: block x of 20 is (token tile, step).  Held relative to the largest decay factor (1
-      // unless a state grows) and times 2^10 (fp16's range)
+      // unless a state grows, see kMaxGrowth) and times 2^10 (fp16's range)
       const float pm = s_pm[team];
       for (int x = tw; x < GdnTP::kBlocks; x += 4) {
         const int half = x < 2 ? 0 : x < 6 ? 1 : x < 12 ? 2 : 3;
@@ -655,8 +660,8 @@ __global__ void __launch_bounds__(kChunkThreads, DK == 256 ? 1 : 3) k_gdn_chunk(
         tp->t_scale = down;
         tp->p_scale = ex2(pm) * 0x1p-10f;
         tp->wd_scale = downw;
-        // (the rule contracts for 0 <= beta <= 2: |T'| <= 4; far above it the writes could overflow)
-        tp->plain = s_plain[team] | s_plain[2] | !(t_max < 0x1p64f);
+        // (the rule contracts for 0 <= beta <= 2: |T'| <= 4.  Far above it the writes grow as a state may.)
+        tp->plain = s_plain[team] | s_plain[2] | !(t_max < 0x1p10f);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -698,7 +703,8 @@ __device__ __forceinline__ void slab_sync(int slab, int threads) {
 __device__ __forceinline__ float4 cat(const float2 (&d)[2]) { return make_float4(d[0].x, d[0].y, d[1].x, d[1].y); }
 
 // Chunk c of a slab, its tokens one by one in fp32, as the decode step does them (k_gdn_step): for chunks
-// with infinities or NaN, which then reach the tokens behind them alone.  All of the slab's warps call it;
+// with infinities or NaN, which then reach the tokens behind them alone, and chunks that grow too far
+// (kMaxGrowth).  All of the slab's warps call it;
 // xch: its exchange area.  (1.6 us a token, where the chunk takes 3 us in one go; that every chunk can come
 // here costs the others 1 to 2 %: 16 x 1024 tokens 549 -> 562 us, 1 x 8192 437 -> 441.)
 template <int DK, int NS>

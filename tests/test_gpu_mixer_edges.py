@@ -271,3 +271,25 @@ def test_writes_far_apart_in_one_chunk(order, big):
     assert (abs(gdn.f64(out) - o) <= bar).all()
     bar = 2.0 ** -14 * m + 2.0 ** -30 * top * 128 ** 0.5
     assert (abs(S[0].double().cpu().numpy() - S_ref) <= bar[..., None]).all()
+
+
+@pytest.mark.parametrize("g", [0.05, 0.15, 0.2, 0.4, 1.3, 1.4])
+def test_prompt_states_that_grow(g):
+    """Growth by e^(64 g) inside a chunk, up to what fp32 holds: the tokens before it keep their bars."""
+    c = gdn.make(2, 4, 128, 40, [64, 20], seed=59)
+    c["g"].fill_(g)
+    c["v"] *= 1e-10
+    c["S"] *= 1e-10
+    out, S, ws = gdn.run(c)
+    assert abi.moe_ws_check(ws) == 0 and torch.isfinite(S).all()
+    gdn.check(c, out, S)
+
+
+@pytest.mark.parametrize("beta", [2.0, 20.0, 3000.0])
+def test_prompt_writes_that_overshoot(beta):
+    """beta of 2 and above, where the rule stops contracting, at two tokens of a chunk."""
+    c = gdn.make(2, 4, 128, 40, [64, 20], seed=60)
+    c["beta"][[3, 50, 70]] = beta
+    out, S, ws = gdn.run(c)
+    assert abi.moe_ws_check(ws) == 0
+    gdn.check(c, out, S)
