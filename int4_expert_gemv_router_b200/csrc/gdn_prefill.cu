@@ -292,8 +292,8 @@ __device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
 constexpr int kChunkThreads = 256;  // four warps per value head, two value heads at a time
 constexpr int kHeadThreads = 128;
 // log2 of how far a state may grow in a chunk (g > 0).  P is held relative to the largest factor, in fp16
-// times 2^10, and a row's W relative to its largest token: what comes before a growth of 2^16 still has
-// steps of 2^-19 and 2^-22 of its own size, and loses a bit with every doubling.  Beyond it the tokens
+// times 2^10, and a row's W relative to its largest token: what comes before a growth of 2^16 is still
+// rounded by 2^-19 and 2^-22 of its own size, and loses a bit with every doubling.  Beyond it the tokens
 // go one by one.
 constexpr float kMaxGrowth = 16.f;
 constexpr int kMatLd = 68;          // row stride (floats) of the 64 x 64 matrices: 16-byte rows
